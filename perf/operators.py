@@ -1,0 +1,463 @@
+"""Measured cases of the operators around a layer's two projections:
+
+  mm     the FP8 products with bias, activation and residual in their epilogue
+         (per-row / per-column scales, and MX block scales)
+  qk     RMS norm of every query and key head with the position rotation
+  write  quantising keys and values into a paged FP8 cache
+  read   reading a batch's pages back as bf16
+  fused  qk and write in one pass, as a decode or prefill step uses them
+
+With ``own`` false ``run`` computes a case with elementary torch operations in
+fp32, rounded once at the end; with ``own`` true it calls the library.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+ACTIVATIONS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+
+
+def listed():
+    return [
+        # one token's attention output projected back into the residual stream
+        mm("mm_one_token", "fp8", 1, 7168, 7168, "none", True, True),
+        # a decode batch through an up projection
+        mm("mm_decode", "fp8", 64, 16384, 7168, "gelu_tanh", True, False),
+        # prefill at the benchmark's largest hidden size, everything in the epilogue
+        mm("mm_prefill", "fp8", 8192, 8192, 8192, "gelu", True, True),
+        # an odd batch against a narrow, short product: the epilogue's share is largest
+        mm("mm_mx_odd", "mx", 1999, 2576, 1024, "silu", True, True),
+        # a prefill's heads, full rotation
+        heads("qk_prefill", "qk", 8192, 64, 8, 128, 128, False, 0.0, 32768),
+        # odd head size, partial adjacent-pair rotation, unit-offset weights
+        heads("qk_odd", "qk", 37, 12, 3, 80, 32, True, 1.0, 4096),
+        # one new token for each sequence of a padded decode batch
+        cache("write_decode", 64, 5, 8, 128, 16, "nhd"),
+        # a long prompt, pages of one head each contiguous
+        cache("write_prompt", 32768, 0, 8, 128, 64, "hnd"),
+        # a few short sequences, one of them empty
+        pages("read_short", 5, 83, 2, 64, 16, "nhd", 3),
+        # long contexts for a prefill that continues them
+        pages("read_long", 48, 131072, 8, 128, 64, "nhd", 100),
+        # a single token's step: latency
+        heads("fused_one_token", "fused", 1, 56, 8, 128, 128, False, 0.0, 32768),
+        # a prefill step
+        heads("fused_prefill", "fused", 8192, 64, 8, 128, 128, False, 0.0, 32768),
+    ]
+
+
+def mm(name, scaling, m, n, k, activation, bias, residual):
+    return dict(name=name, op="mm", scaling=scaling, m=m, n=n, k=k, activation=activation,
+                bias=bias, residual=residual)
+
+
+def heads(name, op, tokens, q_heads, kv_heads, dim, rot, interleaved, offset, positions):
+    return dict(name=name, op=op, tokens=tokens, q_heads=q_heads, kv_heads=kv_heads, dim=dim,
+                rot=rot, interleaved=interleaved, offset=offset, positions=positions, page=16,
+                layout="nhd", padded=tokens // 16 if op == "fused" else 0)
+
+
+def cache(name, tokens, padded, kv_heads, dim, page, layout):
+    return dict(name=name, op="write", tokens=tokens, padded=padded, kv_heads=kv_heads, dim=dim,
+                page=page, layout=layout)
+
+
+def pages(name, sequences, total, kv_heads, dim, page, layout, spare):
+    return dict(name=name, op="read", sequences=sequences, total=total, kv_heads=kv_heads,
+                dim=dim, page=page, layout=layout, spare=spare)
+
+
+def draw(rng):
+    def log(lo, hi):
+        return min(hi, max(lo, round(math.exp(rng.uniform(math.log(lo), math.log(hi))))))
+
+    op = rng.choice(("mm", "mm", "qk", "write", "read", "fused"))
+    dim = rng.choice((64, 80, 96, 128, 128, 192, 256))
+    kv_heads = rng.randint(1, 8)
+    page = rng.choice((1, 16, 24, 64, 128))
+    layout = rng.choice(("nhd", "hnd"))
+    if op == "mm":
+        scaling = rng.choice(("fp8", "mx"))
+        k = 128 * log(1, 64) if scaling == "mx" else 16 * log(8, 512)
+        case = mm("", scaling, log(1, 8192), 16 * log(16, 512), k, rng.choice(ACTIVATIONS),
+                  rng.random() < 0.7, rng.random() < 0.7)
+    elif op == "write":
+        tokens = log(1, 32768)
+        case = cache("", tokens, rng.randint(0, tokens // 2), kv_heads, dim, page, layout)
+    elif op == "read":
+        total = log(1, 131072)
+        dim = min(dim, 128)
+        case = pages("", rng.randint(1, 64), total, kv_heads, dim, page, layout,
+                     rng.randint(0, 200))
+    else:
+        rot = rng.choice((dim, 16 * max(1, dim // 32)))
+        case = heads("", op, log(1, 8192), kv_heads * rng.randint(1, 8), kv_heads, dim, rot,
+                     rng.random() < 0.5, rng.choice((0.0, 1.0)), rng.choice((8192, 32768)))
+        case.update(page=page, layout=layout)
+    del case["name"]
+    return case
+
+
+def work(case):
+    c = case
+    if c["op"] == "mm":
+        m, n, k = c["m"], c["n"], c["k"]
+        scales = 4 * (m + n) if c["scaling"] == "fp8" else (m + n) * (k // 32)
+        return {"bytes": m * k + n * k + scales + 2 * n * c["bias"] +
+                2 * m * n * (2 if c["residual"] else 1), "flops": 2 * m * n * k}
+    kv = c["kv_heads"] * c["dim"]  # values of one token's keys
+    if c["op"] == "read":
+        per = 2 * (kv + 4 * c["kv_heads"] + 2 * kv)
+        return {"bytes": c["total"] * per + 4 * table_entries(c), "flops": 2 * c["total"] * kv}
+    if c["op"] == "write":
+        real = c["tokens"] - c["padded"]
+        return {"bytes": real * 2 * (2 * kv + kv + 4 * c["kv_heads"]) + 8 * c["tokens"],
+                "flops": 4 * real * kv}
+    t, q = c["tokens"], c["q_heads"] * c["dim"]
+    table = 4 * c["rot"] * min(t, c["positions"])
+    norm = 2 * t * 2 * q + 4 * c["dim"] + 8 * t + table
+    if c["op"] == "qk":
+        return {"bytes": norm + 2 * t * 2 * kv, "flops": 8 * t * (q + kv)}
+    real = t - c["padded"]
+    return {"bytes": norm + real * 2 * (2 * kv + kv + 4 * c["kv_heads"]) + 8 * t,
+            "flops": 8 * t * (q + kv)}
+
+
+def table_entries(c):
+    return sum(-(-n // c["page"]) for n in lengths(c))
+
+
+def lengths(c):
+    """The sequences' lengths: uneven, some zero, `total` in all."""
+    rng = random.Random(c["sequences"] * 1000003 + c["total"])
+    weights = [0.0 if rng.random() < 0.1 else rng.expovariate(1.0) for _ in range(c["sequences"])]
+    weights[0] += 0.5
+    whole = [int(c["total"] * w / sum(weights)) for w in weights]
+    whole[-1] += c["total"] - sum(whole)
+    return whole
+
+
+# ------------------------------------------------------------------ inputs --
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    c = dict(case)
+    return {"c": c, **{"mm": prepare_mm, "qk": prepare_heads, "fused": prepare_heads,
+                       "write": prepare_write, "read": prepare_read}[c["op"]](c, g)}
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda", dtype=torch.float32)
+
+
+def rows_fp8(x):
+    """Codes and one scale per row."""
+    scale = x.abs().amax(dim=1) / 448
+    return (x / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn), scale
+
+
+def rows_mx(x):
+    """Codes and one power-of-two scale code per 32 values, the scale codes in
+    the order the block-scaled product takes."""
+    r, k = x.shape
+    exponent = torch.floor(torch.log2(x.view(r, k // 32, 32).abs().amax(dim=2))) - 8
+    code = (exponent + 127).clamp(0, 254)
+    value = x / torch.exp2(code - 127).repeat_interleave(32, dim=1)
+    block = torch.zeros((-(-r // 128) * 128, k // 32), dtype=torch.uint8, device=x.device)
+    block[:r] = code.to(torch.uint8)
+    block = block.view(-1, 4, 32, k // 128, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+    return value.clamp(-448, 448).to(torch.float8_e4m3fn), block.contiguous()
+
+
+def prepare_mm(c, g):
+    quantise = rows_fp8 if c["scaling"] == "fp8" else rows_mx
+    # normalised activations against a weight that keeps their size
+    a, sa = quantise(randn(g, c["m"], c["k"]))
+    b, sb = quantise(randn(g, c["n"], c["k"]) / math.sqrt(c["k"]))
+    bias = (0.5 * randn(g, c["n"])).bfloat16() if c["bias"] else None
+    residual = randn(g, c["m"], c["n"]).bfloat16() if c["residual"] else None
+    return dict(a=a, sa=sa, b=b, sb=sb, bias=bias, residual=residual)
+
+
+def prepare_heads(c, g):
+    t, d, hq, hk = c["tokens"], c["dim"], c["q_heads"], c["kv_heads"]
+    # one projection's output: queries, keys and values of a token side by side
+    qkv = randn(g, t, hq + 2 * hk, d).mul_(1.5).bfloat16()
+    gamma = [(0.1 * randn(g, d) + 1.0 - c["offset"]).bfloat16() for _ in range(2)]
+    half = c["rot"] // 2
+    freq = 10000.0 ** (-torch.arange(half, device="cuda", dtype=torch.float64) / half)
+    angle = torch.arange(c["positions"], device="cuda", dtype=torch.float64)[:, None] * freq
+    table = torch.cat((angle.cos(), angle.sin()), dim=1).float()
+    # runs of up to 512 consecutive positions, each anywhere in its context
+    i = torch.arange(t, device="cuda")
+    begin = torch.randint(c["positions"] - 511, (t // 512 + 1,), generator=g, device="cuda")
+    position = begin[i // 512] + i % 512
+    s = dict(q=qkv[:, :hq], k=qkv[:, hq:hq + hk], v=qkv[:, hq + hk:], q_gamma=gamma[0],
+             k_gamma=gamma[1], eps=1e-6, cos_sin=table, positions=position)
+    return {**s, **new_cache(c, g, t)} if c["op"] == "fused" else s
+
+
+def prepare_write(c, g):
+    kv = randn(g, c["tokens"], 2 * c["kv_heads"], c["dim"]).bfloat16()
+    return dict(k=kv[:, :c["kv_heads"]], v=kv[:, c["kv_heads"]:], **new_cache(c, g, c["tokens"]))
+
+
+def new_cache(c, g, tokens):
+    """A cache that holds earlier tokens, and the slots of `tokens` new ones:
+    pages anywhere, the tokens of a page in order, the batch's padding last."""
+    used = -(-tokens // c["page"])
+    count = used + used // 4 + 3
+    s = filled(c, g, count)
+    page = torch.randperm(count, generator=g, device="cuda")
+    i = torch.arange(tokens, device="cuda")
+    slots = page[i // c["page"]] * c["page"] + i % c["page"]
+    real = tokens - c["padded"]
+    slots[real:] = -1
+    return dict(slots=slots, real=real, scale_ub=1200.0, **s)
+
+
+def filled(c, g, count):
+    h, d, p = c["kv_heads"], c["dim"], c["page"]
+    s = {}
+    for name in "kv":
+        codes = (100 * randn(g, count, p, h, d)).clamp(-448, 448).to(torch.float8_e4m3fn)
+        if c["layout"] == "hnd":
+            codes = codes.view(count, h, p, d).transpose(1, 2)
+        s[name + "_cache"] = codes
+        scales = torch.rand((count, p, h), generator=g, device="cuda") * 0.01 + 0.001
+        s[name + "_scales"] = scales
+    return s
+
+
+def prepare_read(c, g):
+    lens, p = lengths(c), c["page"]
+    need = [-(-n // p) for n in lens]
+    count = sum(need) + 3
+    s = filled(c, g, count)
+    order = torch.randperm(count, generator=g, device="cuda").int()
+    # a row per sequence; entries behind a sequence's pages name no page
+    width = max(need)
+    row = torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(need))
+    first = torch.tensor([0] + need[:-1]).cumsum(0)
+    column = torch.arange(sum(need)) - first[row]
+    table = torch.full((len(lens), width), -1, dtype=torch.int32, device="cuda")
+    table[row.cuda(), column.cuda()] = order[: sum(need)]
+    starts = torch.tensor([0] + lens).cumsum(0).int().cuda()
+    rows = c["total"] + c["spare"]
+    out = [torch.zeros((rows, c["kv_heads"], c["dim"]), dtype=torch.bfloat16, device="cuda")
+           for _ in range(2)]
+    return dict(block_table=table, seq_starts=starts, k_out=out[0], v_out=out[1], **s)
+
+
+# --------------------------------------------------------------------- run --
+
+
+def run(state):
+    return (run_own if own else run_plain)(state)
+
+
+def run_own(s):
+    import reduce_rmsnorm_fp8_b200 as rrf
+    c = s["c"]
+    if c["op"] == "mm":
+        call = rrf.rrf_scaled_mm_fp8_act if c["scaling"] == "fp8" else rrf.rrf_scaled_mm_mxfp8_act
+        return call(s["a"], s["sa"], s["b"], s["sb"], bias=s["bias"], activation=c["activation"],
+                    residual=s["residual"])
+    if c["op"] == "qk":
+        return rrf.rrf_qk_norm_rope(s["q"], s["k"], s["q_gamma"], s["k_gamma"], s["eps"],
+                                    c["offset"], s["cos_sin"], s["positions"],
+                                    interleaved=c["interleaved"])
+    store = (s["k_cache"], s["k_scales"], s["v_cache"], s["v_scales"])
+    if c["op"] == "read":
+        return rrf.rrf_kv_cache_read_fp8(*store, s["block_table"], s["seq_starts"], s["k_out"],
+                                         s["v_out"])
+    if c["op"] == "write":
+        rrf.rrf_kv_cache_write_fp8(s["k"], s["v"], s["slots"], *store, scale_ub=s["scale_ub"])
+        return store
+    q = rrf.rrf_qk_norm_rope_kv_cache_fp8(s["q"], s["k"], s["v"], s["q_gamma"], s["k_gamma"],
+                                          s["eps"], c["offset"], s["cos_sin"], s["positions"],
+                                          s["slots"], *store, scale_ub=s["scale_ub"],
+                                          interleaved=c["interleaved"])
+    return (q, *store)
+
+
+def run_plain(s):
+    c = s["c"]
+    if c["op"] == "mm":
+        return plain_mm(s)
+    if c["op"] == "qk":
+        return (plain_head(s, s["q"], s["q_gamma"]).bfloat16(),
+                plain_head(s, s["k"], s["k_gamma"]).bfloat16())
+    store = (s["k_cache"], s["k_scales"], s["v_cache"], s["v_scales"])
+    if c["op"] == "read":
+        return plain_read(s)
+    if c["op"] == "write":
+        plain_write(s, s["k"].float(), s["v"].float())
+        return store
+    plain_write(s, plain_head(s, s["k"], s["k_gamma"]), s["v"].float())
+    return (plain_head(s, s["q"], s["q_gamma"]).bfloat16(), *store)
+
+
+def plain_mm(s):
+    c = s["c"]
+    a, b = s["a"].float(), s["b"].float()
+    if c["scaling"] == "mx":
+        y = (a * plain_scales(s["sa"], *a.shape)) @ (b * plain_scales(s["sb"], *b.shape)).T
+    else:
+        y = a @ b.T * s["sa"][:, None] * s["sb"]
+    if c["bias"]:
+        y = y + s["bias"].float()
+    act = c["activation"]
+    if act == "relu":
+        y = y.clamp(min=0)
+    elif act == "gelu":
+        y = 0.5 * y * (1 + torch.erf(y * math.sqrt(0.5)))
+    elif act == "gelu_tanh":
+        y = 0.5 * y * (1 + torch.tanh(math.sqrt(2 / math.pi) * (y + 0.044715 * y * y * y)))
+    elif act == "silu":
+        y = y / (1 + torch.exp(-y))
+    if c["residual"]:
+        y = y + s["residual"].float()
+    return y.bfloat16()
+
+
+def plain_scales(block, r, k):
+    code = block.view(-1, k // 128, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(-1, k // 32)[:r]
+    return torch.exp2(code.float() - 127).repeat_interleave(32, dim=1)
+
+
+def plain_head(s, x, gamma):
+    """Norm and rotation of [tokens, heads, dim], in fp32."""
+    c = s["c"]
+    x = x.float()
+    x = x * torch.rsqrt((x * x).mean(dim=-1, keepdim=True) + s["eps"])
+    x = x * (gamma.float() + c["offset"])
+    half = c["rot"] // 2
+    cos, sin = s["cos_sin"][s["positions"]][:, None].split(half, dim=-1)
+    turned, rest = x[..., : c["rot"]], x[..., c["rot"]:]
+    if c["interleaved"]:
+        u, w = turned[..., 0::2], turned[..., 1::2]
+        turned = torch.stack((u * cos - w * sin, w * cos + u * sin), dim=-1).flatten(-2)
+    else:
+        u, w = turned[..., :half], turned[..., half:]
+        turned = torch.cat((u * cos - w * sin, w * cos + u * sin), dim=-1)
+    return torch.cat((turned, rest), dim=-1)
+
+
+def plain_write(s, k, v):
+    c, real = s["c"], s["real"]
+    slot = s["slots"][:real]
+    page, place = slot // c["page"], slot % c["page"]
+    for name, x in (("k", k[:real]), ("v", v[:real])):
+        scale = x.abs().amax(dim=-1).clamp(max=s["scale_ub"]).clamp(min=1e-12) / 448
+        code = (x / scale[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        s[name + "_cache"].view(torch.uint8)[page, place] = code.view(torch.uint8)
+        s[name + "_scales"][page, place] = scale
+
+
+def plain_read(s):
+    c, starts = s["c"], s["seq_starts"].long()
+    row = torch.arange(c["total"], device="cuda")
+    sequence = torch.searchsorted(starts, row, right=True) - 1
+    at = row - starts[sequence]
+    page, place = s["block_table"][sequence, at // c["page"]].long(), at % c["page"]
+    for name in "kv":
+        code = s[name + "_cache"].view(torch.uint8)[page, place].view(torch.float8_e4m3fn)
+        value = code.float() * s[name + "_scales"][page, place][..., None]
+        s[name + "_out"][: c["total"]] = value.bfloat16()
+    return s["k_out"], s["v_out"]
+
+
+# ------------------------------------------------------------------- exact --
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    c = s["c"]
+    if c["op"] == "mm":
+        return exact_mm(s)
+    if c["op"] == "read":
+        return exact_read(s)
+    if c["op"] == "qk":
+        return exact_head(s, "q"), exact_head(s, "k")
+    if c["op"] == "write":
+        return exact_write(s, s["k"].double(), s["v"].double())
+    return (exact_head(s, "q"), *exact_write(s, exact_head(s, "k"), s["v"].double()))
+
+
+def exact_mm(s):
+    c = s["c"]
+    a, b = s["a"].double(), s["b"].double()
+    if c["scaling"] == "mx":
+        for x, block in ((a, s["sa"]), (b, s["sb"])):
+            # row r, scale j: byte (r % 32) * 16 + (r // 32 % 4) * 4 + j % 4 of
+            # the 512 of row block r // 128 and column block j // 4
+            r = torch.arange(x.shape[0], device="cuda")[:, None]
+            j = torch.arange(c["k"] // 32, device="cuda")[None, :]
+            byte = ((r // 128) * (c["k"] // 128) + j // 4) * 512 + r % 32 * 16 + r // 32 % 4 * 4
+            scale = torch.pow(2.0, block[byte + j % 4].double() - 127)
+            x.view(x.shape[0], -1, 32).mul_(scale[..., None])
+        y = torch.matmul(a, b.mT)
+    else:
+        y = torch.matmul(a * s["sa"].double()[:, None], (b * s["sb"].double()[:, None]).mT)
+    if s["bias"] is not None:
+        y += s["bias"].double()
+    y = {"none": lambda x: x, "relu": torch.relu, "silu": torch.nn.functional.silu,
+         "gelu": torch.nn.functional.gelu,
+         "gelu_tanh": lambda x: torch.nn.functional.gelu(x, approximate="tanh"),
+         }[c["activation"]](y)
+    return y if s["residual"] is None else y + s["residual"].double()
+
+
+def exact_head(s, name):
+    c = s["c"]
+    x = s[name].double()
+    norm = torch.sqrt(x.pow(2).sum(-1, keepdim=True) / c["dim"] + s["eps"])
+    y = x / norm * (s[name + "_gamma"].double() + c["offset"])
+    half = c["rot"] // 2
+    row = s["cos_sin"].double()[s["positions"]][:, None, :]
+    turn = torch.complex(row[..., :half], row[..., half:])
+    i = torch.arange(half, device="cuda")
+    first, second = (2 * i, 2 * i + 1) if c["interleaved"] else (i, i + half)
+    z = torch.complex(y[..., first], y[..., second]) * turn
+    out = y.clone()
+    out[..., first], out[..., second] = z.real, z.imag
+    return out
+
+
+def exact_write(s, k, v):
+    c = s["c"]
+    got = []
+    for name, x in (("k", k), ("v", v)):
+        codes, scales = s[name + "_cache"].double(), s[name + "_scales"].double()
+        keep = s["slots"] >= 0
+        slot, x = s["slots"][keep], x[keep]
+        scale = x.abs().amax(-1).clamp(max=s["scale_ub"]).clamp(min=1e-12) / 448
+        y = x / scale[..., None]
+        # the e4m3 grid: 8 steps to a power of two, 2^-9 apart below 2^-6
+        step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
+        page, place = torch.div(slot, c["page"], rounding_mode="floor"), slot % c["page"]
+        codes[page, place] = (torch.round(y / step) * step).clamp(-448, 448)
+        scales[page, place] = scale
+        got += [codes, scales]
+    return tuple(got)
+
+
+def exact_read(s):
+    c, got = s["c"], []
+    lens = torch.tensor(lengths(c))
+    sequence = torch.repeat_interleave(torch.arange(len(lens)), lens)
+    at = torch.arange(c["total"]) - (lens.cumsum(0) - lens)[sequence]
+    page = s["block_table"].cpu()[sequence, at // c["page"]].long().cuda()
+    place = (at % c["page"]).cuda()
+    for name in "kv":
+        out = s[name + "_out"].double()
+        value = s[name + "_cache"].double()[page, place]
+        out[: c["total"]] = value * s[name + "_scales"].double()[page, place][..., None]
+        got.append(out)
+    return tuple(got)
