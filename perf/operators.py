@@ -437,8 +437,11 @@ def exact_write(s, k, v):
         codes, scales = s[name + "_cache"].double(), s[name + "_scales"].double()
         keep = s["slots"] >= 0
         slot, x = s["slots"][keep], x[keep]
-        scale = x.abs().amax(-1).clamp(max=s["scale_ub"]).clamp(min=1e-12) / 448
-        y = x / scale[..., None]
+        most = x.abs().amax(-1).clamp(max=s["scale_ub"]).clamp(min=1e-12)
+        scale = most / 448
+        # x / scale with one rounding: with two, the midpoints that short
+        # mantissas often hit would land on either side
+        y = x * 448 / most[..., None]
         # the e4m3 grid: 8 steps to a power of two, 2^-9 apart below 2^-6
         step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
         page, place = torch.div(slot, c["page"], rounding_mode="floor"), slot % c["page"]
