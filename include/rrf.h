@@ -544,6 +544,157 @@ rrf_status rrf_plan_scaled_mm(int64_t M, int64_t N, int64_t K, int mx, int sm_co
                               int* kernel, int* a_rows, int* tile_n, int* k_tiles_per_stage,
                               int64_t* tiles, int64_t* ctas);
 
+/* ------------------------------------------------------------------------
+ * Between the projection and the attention of a layer: the norm of every
+ * query and key head with the position rotation, and an FP8 cache of keys
+ * and values.
+ *
+ * One head x of head_dim values (fp32 throughout, rounded once when stored):
+ *   r    = 1 / sqrt(sum_j x_j^2 / head_dim + eps)
+ *   y_j  = (x_j * r) * (gamma_j + weight_offset)
+ *   rotation of the first rot_dim values by the angles of the token's
+ *   position, pair i (i < rot_dim / 2) being (i, i + rot_dim / 2) or, with
+ *   interleaved != 0, (2i, 2i + 1):
+ *     (y_a, y_b) <- (y_a cos_i - y_b sin_i, y_b cos_i + y_a sin_i)
+ * The cache holds one scale per token and head, by the rule of the fused
+ * call's rows:
+ *   scale = max(min(max_j |x_j|, scale_ub), 1e-12) / 448
+ *   q_j   = e4m3fn(x_j / scale), nearest even, saturating at +-448
+ * A NaN does not count in the maximum and is stored as the NaN code; an
+ * infinity counts (cut to scale_ub; without one the row's finite values
+ * become 0 and the infinities NaN).
+ *
+ * The arrays of heads are bf16 [tokens, heads, head_dim] with the head's
+ * values contiguous and any token and head strides (in elements, multiples
+ * of 8), so the parts of a projection's output are passed as they lie.
+ * Inputs may overlap one another; an output's heads must not overlap one
+ * another, and no output may overlap an input or another output, except
+ * q_out == q and k_out == k with the same strides (in place).  Two arrays
+ * interleaved in one buffer are told apart when they have the same token
+ * (page) stride and each keeps to its own part of it; otherwise arrays whose
+ * extents overlap are refused.
+ *
+ * head_dim: a multiple of 16, 16..512.  rot_dim: a multiple of 16,
+ * 0..head_dim (0: norm alone; cos_sin and positions are not read).
+ * Device data that names a place outside its array never moves an access
+ * there: RRF_DEVICE_ERROR_INDEX is set in the device error word and the token
+ * (a position or slot) or row (a page) is left out, its outputs as they were.
+ * ---------------------------------------------------------------------- */
+
+#define RRF_MAX_HEAD_DIM 512
+
+/* A paged cache of keys and values: e4m3fn codes [num_pages, page_size,
+ * kv_heads, head_dim] and float scales [num_pages, page_size, kv_heads].
+ * Slot s is place s % page_size of page s / page_size.  Strides (page, place,
+ * head) are shared by keys and values, in elements; code strides are multiples
+ * of 16, the codes of a head contiguous, code pointers 16-byte aligned and
+ * scale pointers 4-byte aligned.  The struct is read during the call. */
+typedef struct rrf_kv_cache {
+    void* k_codes;
+    float* k_scales;
+    void* v_codes;
+    float* v_scales;
+    int64_t num_pages;
+    int64_t page_size;
+    int64_t code_strides[3];
+    int64_t scale_strides[3];
+} rrf_kv_cache;
+
+/* rrf_qk_norm_rope -- norm and rotation of queries and keys.
+ * q, k          bf16 [tokens, q_heads / kv_heads, head_dim], 16-byte aligned
+ * *_token, *_head  strides of the array before them, in elements
+ * q_out, k_out  the same shapes
+ * q_gamma, k_gamma  bf16 [head_dim], 16-byte aligned
+ * cos_sin       float [max_positions, rot_dim]: rot_dim / 2 cosines, then
+ *               rot_dim / 2 sines; 16-byte aligned
+ * positions     int64 [tokens], each in [0, max_positions); 8-byte aligned
+ * tokens == 0 is a no-op.
+ * Errors: RRF_ERR_NULL, RRF_ERR_SHAPE, RRF_ERR_ALIGN (pointers and strides),
+ *         RRF_ERR_ALIAS, RRF_ERR_VALUE, RRF_ERR_CUDA. */
+rrf_status rrf_qk_norm_rope(const void* q, int64_t q_token, int64_t q_head, const void* k,
+                            int64_t k_token, int64_t k_head, void* q_out, int64_t q_out_token,
+                            int64_t q_out_head, void* k_out, int64_t k_out_token,
+                            int64_t k_out_head, const void* q_gamma, const void* k_gamma,
+                            float eps, float weight_offset, const float* cos_sin,
+                            int64_t max_positions, int64_t rot_dim, int interleaved,
+                            const int64_t* positions, int64_t tokens, int64_t q_heads,
+                            int64_t kv_heads, int64_t head_dim, rrf_stream_t stream);
+
+/* rrf_kv_cache_write_fp8 -- quantise keys and values into their slots.
+ * k, v      bf16 [tokens, kv_heads, head_dim], 16-byte aligned
+ * slots     int64 [tokens], 8-byte aligned; a negative slot is a padding
+ *           token, which is not stored.  The other slots must differ: what a
+ *           slot holds that is named twice is unspecified (other slots are
+ *           not touched).
+ * scale_ub  > 0 (may be +inf: no clamp)
+ * Errors: as rrf_qk_norm_rope. */
+rrf_status rrf_kv_cache_write_fp8(const void* k, int64_t k_token, int64_t k_head, const void* v,
+                                  int64_t v_token, int64_t v_head, const int64_t* slots,
+                                  float scale_ub, const rrf_kv_cache* cache, int64_t tokens,
+                                  int64_t kv_heads, int64_t head_dim, rrf_stream_t stream);
+
+/* rrf_qk_norm_rope_kv_cache_fp8 -- both in one pass: queries as
+ * rrf_qk_norm_rope writes them, keys (from their fp32 values, not rounded to
+ * bf16 between) and values into the cache.  Queries are written for padding
+ * tokens too. */
+rrf_status rrf_qk_norm_rope_kv_cache_fp8(
+    const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+    int64_t k_head, const void* v, int64_t v_token, int64_t v_head, void* q_out,
+    int64_t q_out_token, int64_t q_out_head, const void* q_gamma, const void* k_gamma, float eps,
+    float weight_offset, const float* cos_sin, int64_t max_positions, int64_t rot_dim,
+    int interleaved, const int64_t* positions, const int64_t* slots, float scale_ub,
+    const rrf_kv_cache* cache, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+    int64_t head_dim, rrf_stream_t stream);
+
+/* rrf_kv_cache_read_fp8 -- a batch's keys and values as bf16, packed:
+ *   out[seq_starts[s] + t] = RN_bf16(code * scale) of slot t % page_size of
+ *   page block_table[s][t / page_size], for seq_starts[s] <= row <
+ *   seq_starts[s + 1].
+ * block_table   int32 [sequences, table_width], rows table_stride apart,
+ *               4-byte aligned; entries behind a sequence's last page are not
+ *               read; a page may be named by several sequences
+ * seq_starts    int32 [sequences + 1], not decreasing, 4-byte aligned
+ * k_out, v_out  bf16 [rows, kv_heads, head_dim], contiguous, 16-byte aligned;
+ *               rows no sequence covers are left as they were, and what a
+ *               sequence has behind `rows` is not written
+ * rows == 0 and sequences == 0 are no-ops.
+ * Errors: RRF_ERR_NULL, RRF_ERR_SHAPE, RRF_ERR_ALIGN, RRF_ERR_ALIAS,
+ *         RRF_ERR_CUDA. */
+rrf_status rrf_kv_cache_read_fp8(const rrf_kv_cache* cache, const int32_t* block_table,
+                                 int64_t table_stride, int64_t table_width,
+                                 const int32_t* seq_starts, int64_t sequences, void* k_out,
+                                 void* v_out, int64_t rows, int64_t kv_heads, int64_t head_dim,
+                                 rrf_stream_t stream);
+
+/* The host validation of these calls alone (no GPU needed). */
+rrf_status rrf_check_qk_norm_rope_args(const void* q, int64_t q_token, int64_t q_head,
+                                       const void* k, int64_t k_token, int64_t k_head,
+                                       const void* q_out, int64_t q_out_token,
+                                       int64_t q_out_head, const void* k_out,
+                                       int64_t k_out_token, int64_t k_out_head,
+                                       const void* q_gamma, const void* k_gamma, float eps,
+                                       float weight_offset, const float* cos_sin,
+                                       int64_t max_positions, int64_t rot_dim,
+                                       const int64_t* positions, int64_t tokens,
+                                       int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+rrf_status rrf_check_kv_cache_write_args(const void* k, int64_t k_token, int64_t k_head,
+                                         const void* v, int64_t v_token, int64_t v_head,
+                                         const int64_t* slots, float scale_ub,
+                                         const rrf_kv_cache* cache, int64_t tokens,
+                                         int64_t kv_heads, int64_t head_dim);
+rrf_status rrf_check_qk_norm_rope_kv_cache_args(
+    const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+    int64_t k_head, const void* v, int64_t v_token, int64_t v_head, const void* q_out,
+    int64_t q_out_token, int64_t q_out_head, const void* q_gamma, const void* k_gamma, float eps,
+    float weight_offset, const float* cos_sin, int64_t max_positions, int64_t rot_dim,
+    const int64_t* positions, const int64_t* slots, float scale_ub, const rrf_kv_cache* cache,
+    int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+rrf_status rrf_check_kv_cache_read_args(const rrf_kv_cache* cache, const int32_t* block_table,
+                                        int64_t table_stride, int64_t table_width,
+                                        const int32_t* seq_starts, int64_t sequences,
+                                        const void* k_out, const void* v_out, int64_t rows,
+                                        int64_t kv_heads, int64_t head_dim);
+
 /* rrf_plan_fused -- the launch rrf_sum_rmsnorm_fp8 would use on a GPU with
  * sm_count SMs for a call with (residual != 0) or without a residual,
  * without touching the GPU.  Writes the cluster size (1 = one
@@ -587,6 +738,8 @@ rrf_status rrf_check_fused_args(const void* const* inputs, int num_inputs, int64
                                       compiled with RRF_DEBUG) found an index
                                       outside its buffer and skipped that
                                       access; never set by the normal build    */
+#define RRF_DEVICE_ERROR_INDEX 16u /* a position, slot or page outside its array
+                                      was left out (the per-head and cache calls) */
 
 /* rrf_device_error -- the device error word of the current device: the OR
  * of RRF_DEVICE_ERROR_* bits that kernels of this library have set since it

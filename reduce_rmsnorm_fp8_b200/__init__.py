@@ -22,6 +22,10 @@ Functions, named after the C entry points:
   rrf_sum_rmsnorm_fp8_pre / rrf_rmsnorm_fp8_post: the two phases of the
       sharded form (a row's hidden dimension split across devices); the
       torch.distributed glue between them is in ``sharded.py``
+  rrf_qk_norm_rope, rrf_kv_cache_write_fp8, rrf_qk_norm_rope_kv_cache_fp8,
+      rrf_kv_cache_read_fp8: the per-head norm and rotation of queries and
+      keys (rope_table makes its table), and a paged FP8 cache of keys and
+      values
 """
 from __future__ import annotations
 
@@ -43,7 +47,9 @@ _EXPORTS = (
     "RRF_AR_STATIC_MAX_WORLD", "rrf_allreduce_rmsnorm_fp8_static_ptr",
     "rrf_plan_scaled_mm", "RRF_GEMM_KERNEL_PAIR", "RRF_GEMM_KERNEL_TILE",
     "RRF_GEMM_KERNEL_SWAP", "RRF_FLAG_NO_PREFETCH", "RRF_FLAG_PREFETCH", "rrf_plan_fused_ex",
-    "RRF_DEVICE_ERROR_BOUNDS",
+    "RRF_DEVICE_ERROR_BOUNDS", "RRF_DEVICE_ERROR_INDEX", "RRF_MAX_HEAD_DIM", "RrfKvCache",
+    "rope_table", "rrf_qk_norm_rope", "rrf_kv_cache_write_fp8", "rrf_kv_cache_read_fp8",
+    "rrf_qk_norm_rope_kv_cache_fp8",
 )
 
 __all__ = list(_EXPORTS)

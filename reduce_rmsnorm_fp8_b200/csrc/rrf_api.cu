@@ -1020,6 +1020,480 @@ extern "C" rrf_status rrf_scaled_mm_mxfp8(const void* a, const void* sa, const v
     return e == cudaSuccess ? RRF_OK : cuda_fail(e);
 }
 
+// ------------------------------------------- heads and the FP8 cache ---
+
+namespace {
+
+// Sizes and strides: no extent comes near 2^63 (checked in 128 bits).
+using Wide = __int128;
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr Wide kMaxExtent = (Wide)1 << 60;
+
+// An array of `n` dimensions around contiguous runs of `width` elements.
+struct Dims {
+    int n;
+    int64_t size[3];
+    int64_t stride[3];
+    int64_t width;
+};
+
+// Elements from the first to behind the last; 0 if it is out of bounds.
+int64_t extent(const Dims& d) {
+    Wide e = d.width;
+    for (int i = 0; i < d.n; ++i) {
+        if (d.size[i] > 1 && (d.stride[i] < 0 || d.stride[i] > kMaxStride)) return 0;
+        if (d.size[i] > 1) e += (Wide)(d.size[i] - 1) * d.stride[i];
+        if (e > kMaxExtent) return 0;
+    }
+    return (int64_t)e;
+}
+
+// No two runs overlap: each stride steps over all that the smaller ones span.
+bool distinct(const Dims& d) {
+    Wide span = d.width;
+    bool done[3] = {};
+    for (int k = 0; k < d.n; ++k) {
+        int next = -1;
+        for (int i = 0; i < d.n; ++i)
+            if (!done[i] && d.size[i] > 1 && (next < 0 || d.stride[i] < d.stride[next])) next = i;
+        if (next < 0) return true;
+        done[next] = true;
+        if (d.stride[next] < span) return false;
+        span += (Wide)(d.size[next] - 1) * d.stride[next];
+    }
+    return true;
+}
+
+// A strided array in memory: bytes [lo, hi), and, for telling interleaved
+// arrays apart, its outer stride and what it spans of one, in bytes.
+struct Region {
+    Range all;
+    int64_t outer;  // 0: one part
+    int64_t part;
+};
+
+Region region_of(const void* p, const Dims& d, int64_t element) {
+    Region r;
+    r.all = range_of(p, extent(d) * element);
+    Dims inner = d;
+    for (int i = 0; i + 1 < d.n; ++i) {
+        inner.size[i] = d.size[i + 1];
+        inner.stride[i] = d.stride[i + 1];
+    }
+    inner.n = d.n - 1;
+    r.outer = d.size[0] > 1 ? d.stride[0] * element : 0;
+    r.part = extent(inner) * element;
+    return r;
+}
+
+Region flat(const void* p, int64_t bytes) { return Region{range_of(p, bytes), 0, bytes}; }
+
+bool overlap(const Region& a, const Region& b) {
+    if (!overlap(a.all, b.all)) return false;
+    if (a.outer == 0 || a.outer != b.outer || a.part > a.outer || b.part > b.outer) return true;
+    // the same outer stride: where b's parts begin within a's
+    const uintptr_t s = (uintptr_t)a.outer;
+    const uintptr_t ab = b.all.lo >= a.all.lo ? (b.all.lo - a.all.lo) % s
+                                              : (s - (a.all.lo - b.all.lo) % s) % s;
+    return ab < (uintptr_t)a.part || s - ab < (uintptr_t)b.part;
+}
+
+// Every write against every read and every other write, except the pairs
+// that are the same array (in place).
+rrf_status check_regions(const Region* writes, int nw, const Region* reads, int nr) {
+    for (int w = 0; w < nw; ++w) {
+        for (int r = 0; r < nr; ++r)
+            if (overlap(writes[w], reads[r])) return RRF_ERR_ALIAS;
+        for (int v = w + 1; v < nw; ++v)
+            if (overlap(writes[w], writes[v])) return RRF_ERR_ALIAS;
+    }
+    return RRF_OK;
+}
+
+struct Heads {
+    const void* p;
+    int64_t token, head, heads;
+};
+
+Dims dims_of(const Heads& h, int64_t tokens, int64_t head_dim) {
+    return Dims{2, {tokens, h.heads, 0}, {h.token, h.head, 0}, head_dim};
+}
+
+HeadView view_of(const Heads& h) {
+    HeadView v = {};
+    v.p = static_cast<uint16_t*>(const_cast<void*>(h.p));
+    v.token_stride = h.token;
+    v.head_stride = h.head;
+    v.heads = (int)h.heads;
+    return v;
+}
+
+rrf_status check_head_shape(int64_t tokens, int64_t heads, int64_t head_dim) {
+    // (a token's chunks and a launch's warps are counted in 32 bits)
+    if (tokens < 0 || tokens > INT32_MAX / 2 || heads < 1 || heads > 4096) return RRF_ERR_SHAPE;
+    if (head_dim < 16 || head_dim > RRF_MAX_HEAD_DIM || head_dim % 16 != 0) return RRF_ERR_SHAPE;
+    return RRF_OK;
+}
+
+rrf_status check_heads(const Heads& h, int64_t tokens, int64_t head_dim, bool output) {
+    if (h.p == nullptr) return RRF_ERR_NULL;
+    const Dims d = dims_of(h, tokens, head_dim);
+    if (extent(d) == 0) return RRF_ERR_SHAPE;
+    if (!aligned(h.p, 16) || (tokens > 1 && h.token % 8 != 0) ||
+        (h.heads > 1 && h.head % 8 != 0))
+        return RRF_ERR_ALIGN;
+    return !output || distinct(d) ? RRF_OK : RRF_ERR_ALIAS;
+}
+
+struct CacheDims {
+    Dims codes, scales;
+};
+
+CacheDims cache_dims(const rrf_kv_cache* c, int64_t kv_heads, int64_t head_dim) {
+    const int64_t* cs = c->code_strides;
+    const int64_t* ss = c->scale_strides;
+    return CacheDims{
+        Dims{3, {c->num_pages, c->page_size, kv_heads}, {cs[0], cs[1], cs[2]}, head_dim},
+        Dims{3, {c->num_pages, c->page_size, kv_heads}, {ss[0], ss[1], ss[2]}, 1}};
+}
+
+rrf_status check_cache(const rrf_kv_cache* c, int64_t kv_heads, int64_t head_dim, bool written,
+                       CacheDims* out) {
+    if (c == nullptr || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales)
+        return RRF_ERR_NULL;
+    if (c->num_pages < 1 || c->num_pages > INT32_MAX || c->page_size < 1 ||
+        c->page_size > INT32_MAX / 2)
+        return RRF_ERR_SHAPE;
+    *out = cache_dims(c, kv_heads, head_dim);
+    if (extent(out->codes) == 0 || extent(out->scales) == 0) return RRF_ERR_SHAPE;
+    for (int i = 0; i < 3; ++i)
+        if (out->codes.size[i] > 1 && c->code_strides[i] % 16 != 0) return RRF_ERR_ALIGN;
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 4) ||
+        !aligned(c->v_scales, 4))
+        return RRF_ERR_ALIGN;
+    if (written && (!distinct(out->codes) || !distinct(out->scales))) return RRF_ERR_ALIAS;
+    return RRF_OK;
+}
+
+int add_cache_regions(const rrf_kv_cache* c, const CacheDims& d, Region* r) {
+    r[0] = region_of(c->k_codes, d.codes, 1);
+    r[1] = region_of(c->v_codes, d.codes, 1);
+    r[2] = region_of(c->k_scales, d.scales, 4);
+    r[3] = region_of(c->v_scales, d.scales, 4);
+    return 4;
+}
+
+rrf_status check_norm(const void* q_gamma, const void* k_gamma, float eps, float weight_offset,
+                      const float* cos_sin, int64_t max_positions, int64_t rot_dim,
+                      const int64_t* positions, int64_t head_dim, bool empty) {
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0) return RRF_ERR_SHAPE;
+    if (rot_dim > 0 && (max_positions < 1 || max_positions > kMaxStride)) return RRF_ERR_SHAPE;
+    if (!(std::isfinite(eps) && eps >= 0.0f) || !std::isfinite(weight_offset))
+        return RRF_ERR_VALUE;
+    if (empty) return RRF_OK;
+    if (!q_gamma || !k_gamma || (rot_dim > 0 && (!cos_sin || !positions))) return RRF_ERR_NULL;
+    if (!aligned(q_gamma, 16) || !aligned(k_gamma, 16)) return RRF_ERR_ALIGN;
+    if (rot_dim > 0 && (!aligned(cos_sin, 16) || !aligned(positions, 8))) return RRF_ERR_ALIGN;
+    return RRF_OK;
+}
+
+// The reads beside the heads: both gammas and, with a rotation, its table
+// and positions.
+int add_norm_regions(const void* q_gamma, const void* k_gamma, const float* cos_sin,
+                     int64_t max_positions, int64_t rot_dim, const int64_t* positions,
+                     int64_t tokens, int64_t head_dim, Region* r) {
+    r[0] = flat(q_gamma, head_dim * 2);
+    r[1] = flat(k_gamma, head_dim * 2);
+    if (rot_dim == 0) return 2;
+    r[2] = flat(cos_sin, max_positions * rot_dim * 4);
+    r[3] = flat(positions, tokens * 8);
+    return 4;
+}
+
+bool same(const Heads& a, const Heads& b, int64_t tokens) {
+    return a.p == b.p && (tokens <= 1 || a.token == b.token) &&
+           (a.heads <= 1 || a.head == b.head);
+}
+
+rrf_status check_scale_ub(float scale_ub) {
+    return std::isnan(scale_ub) || !(scale_ub > 0.0f) ? RRF_ERR_VALUE : RRF_OK;
+}
+
+// A checked cache's part of a call's arguments (HeadsArgs, CacheReadArgs).
+// (The stride of a dimension of one element is only ever taken zero times.)
+template <class Args>
+void set_cache(Args* a, const rrf_kv_cache* c, int64_t kv_heads, int64_t head_dim) {
+    a->k_codes = static_cast<uint8_t*>(c->k_codes);
+    a->v_codes = static_cast<uint8_t*>(c->v_codes);
+    a->k_scales = c->k_scales;
+    a->v_scales = c->v_scales;
+    a->page_size = (int)c->page_size;
+    a->code_page = c->code_strides[0];
+    a->code_slot = c->code_strides[1];
+    a->code_head = c->code_strides[2];
+    a->scale_page = c->scale_strides[0];
+    a->scale_slot = c->scale_strides[1];
+    a->scale_head = c->scale_strides[2];
+    const CacheDims d = cache_dims(c, kv_heads, head_dim);
+    a->code_end = extent(d.codes);
+    a->scale_end = extent(d.scales);
+}
+
+void set_norm(HeadsArgs* a, const void* q_gamma, const void* k_gamma, float eps,
+              float weight_offset, const float* cos_sin, int64_t max_positions, int64_t rot_dim,
+              int interleaved, const int64_t* positions, int64_t tokens, int64_t head_dim) {
+    a->q_gamma = static_cast<const uint4*>(q_gamma);
+    a->k_gamma = static_cast<const uint4*>(k_gamma);
+    a->eps = eps;
+    a->weight_offset = weight_offset;
+    a->cos_sin = cos_sin;
+    a->max_positions = max_positions;
+    a->rot = (int)rot_dim;
+    a->interleaved = interleaved != 0;
+    a->positions = positions;
+    a->tokens = (int)tokens;
+    a->dim = (int)head_dim;
+    a->inv_dim = (float)(1.0 / (double)head_dim);
+}
+
+rrf_status run_heads(HeadsArgs& a, bool norm, rrf_stream_t stream) {
+    int sm_count = 0;
+    rrf_status st = current_sm_count(&sm_count);
+    if (st != RRF_OK) return st;
+    if ((st = device_error_word(&a.err)) != RRF_OK) return st;
+    cudaError_t e;
+    if (!take_injected_failure(&e)) e = launch_heads(a, norm, sm_count, (cudaStream_t)stream);
+    return e == cudaSuccess ? RRF_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" rrf_status rrf_check_qk_norm_rope_args(
+    const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+    int64_t k_head, const void* q_out, int64_t q_out_token, int64_t q_out_head,
+    const void* k_out, int64_t k_out_token, int64_t k_out_head, const void* q_gamma,
+    const void* k_gamma, float eps, float weight_offset, const float* cos_sin,
+    int64_t max_positions, int64_t rot_dim, const int64_t* positions, int64_t tokens,
+    int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    rrf_status st;
+    if ((st = check_head_shape(tokens, q_heads, head_dim)) != RRF_OK) return st;
+    if ((st = check_head_shape(tokens, kv_heads, head_dim)) != RRF_OK) return st;
+    if ((st = check_norm(q_gamma, k_gamma, eps, weight_offset, cos_sin, max_positions, rot_dim,
+                         positions, head_dim, tokens == 0)) != RRF_OK || tokens == 0)
+        return st;
+    const Heads in[2] = {{q, q_token, q_head, q_heads}, {k, k_token, k_head, kv_heads}};
+    const Heads out[2] = {{q_out, q_out_token, q_out_head, q_heads},
+                          {k_out, k_out_token, k_out_head, kv_heads}};
+    Region reads[6], writes[2];
+    for (int i = 0; i < 2; ++i) {
+        if ((st = check_heads(in[i], tokens, head_dim, false)) != RRF_OK) return st;
+        if ((st = check_heads(out[i], tokens, head_dim, true)) != RRF_OK) return st;
+        writes[i] = region_of(out[i].p, dims_of(out[i], tokens, head_dim), 2);
+    }
+    int n = add_norm_regions(q_gamma, k_gamma, cos_sin, max_positions, rot_dim, positions, tokens,
+                             head_dim, reads);
+    for (int i = 0; i < 2; ++i) {
+        const Region r = region_of(in[i].p, dims_of(in[i], tokens, head_dim), 2);
+        if (!same(in[i], out[i], tokens)) reads[n++] = r;
+        else if (overlap(r, writes[1 - i])) return RRF_ERR_ALIAS;
+    }
+    return check_regions(writes, 2, reads, n);
+}
+
+extern "C" rrf_status rrf_qk_norm_rope(
+    const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+    int64_t k_head, void* q_out, int64_t q_out_token, int64_t q_out_head, void* k_out,
+    int64_t k_out_token, int64_t k_out_head, const void* q_gamma, const void* k_gamma, float eps,
+    float weight_offset, const float* cos_sin, int64_t max_positions, int64_t rot_dim,
+    int interleaved, const int64_t* positions, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+    int64_t head_dim, rrf_stream_t stream) {
+    const rrf_status st = rrf_check_qk_norm_rope_args(
+        q, q_token, q_head, k, k_token, k_head, q_out, q_out_token, q_out_head, k_out,
+        k_out_token, k_out_head, q_gamma, k_gamma, eps, weight_offset, cos_sin, max_positions,
+        rot_dim, positions, tokens, q_heads, kv_heads, head_dim);
+    if (st != RRF_OK || tokens == 0) return st;
+    HeadsArgs a = {};
+    a.q = view_of({q, q_token, q_head, q_heads});
+    a.k = view_of({k, k_token, k_head, kv_heads});
+    a.q_out = view_of({q_out, q_out_token, q_out_head, q_heads});
+    a.k_out = view_of({k_out, k_out_token, k_out_head, kv_heads});
+    set_norm(&a, q_gamma, k_gamma, eps, weight_offset, cos_sin, max_positions, rot_dim,
+             interleaved, positions, tokens, head_dim);
+    return run_heads(a, true, stream);
+}
+
+extern "C" rrf_status rrf_check_kv_cache_write_args(const void* k, int64_t k_token,
+                                                    int64_t k_head, const void* v,
+                                                    int64_t v_token, int64_t v_head,
+                                                    const int64_t* slots, float scale_ub,
+                                                    const rrf_kv_cache* cache, int64_t tokens,
+                                                    int64_t kv_heads, int64_t head_dim) {
+    rrf_status st;
+    if ((st = check_head_shape(tokens, kv_heads, head_dim)) != RRF_OK) return st;
+    if ((st = check_scale_ub(scale_ub)) != RRF_OK || tokens == 0) return st;
+    const Heads in[2] = {{k, k_token, k_head, kv_heads}, {v, v_token, v_head, kv_heads}};
+    Region reads[3], writes[4];
+    for (int i = 0; i < 2; ++i) {
+        if ((st = check_heads(in[i], tokens, head_dim, false)) != RRF_OK) return st;
+        reads[i] = region_of(in[i].p, dims_of(in[i], tokens, head_dim), 2);
+    }
+    CacheDims d;
+    if ((st = check_cache(cache, kv_heads, head_dim, true, &d)) != RRF_OK) return st;
+    if (slots == nullptr) return RRF_ERR_NULL;
+    if (!aligned(slots, 8)) return RRF_ERR_ALIGN;
+    reads[2] = flat(slots, tokens * 8);
+    return check_regions(writes, add_cache_regions(cache, d, writes), reads, 3);
+}
+
+extern "C" rrf_status rrf_kv_cache_write_fp8(const void* k, int64_t k_token, int64_t k_head,
+                                             const void* v, int64_t v_token, int64_t v_head,
+                                             const int64_t* slots, float scale_ub,
+                                             const rrf_kv_cache* cache, int64_t tokens,
+                                             int64_t kv_heads, int64_t head_dim,
+                                             rrf_stream_t stream) {
+    const rrf_status st = rrf_check_kv_cache_write_args(k, k_token, k_head, v, v_token, v_head,
+                                                        slots, scale_ub, cache, tokens, kv_heads,
+                                                        head_dim);
+    if (st != RRF_OK || tokens == 0) return st;
+    HeadsArgs a = {};
+    a.k = view_of({k, k_token, k_head, kv_heads});
+    a.v = view_of({v, v_token, v_head, kv_heads});
+    a.slots = slots;
+    a.scale_ub = scale_ub;
+    a.tokens = (int)tokens;
+    a.dim = (int)head_dim;
+    set_cache(&a, cache, kv_heads, head_dim);
+    a.num_slots = cache->num_pages * cache->page_size;
+    return run_heads(a, false, stream);
+}
+
+extern "C" rrf_status rrf_check_qk_norm_rope_kv_cache_args(
+    const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+    int64_t k_head, const void* v, int64_t v_token, int64_t v_head, const void* q_out,
+    int64_t q_out_token, int64_t q_out_head, const void* q_gamma, const void* k_gamma, float eps,
+    float weight_offset, const float* cos_sin, int64_t max_positions, int64_t rot_dim,
+    const int64_t* positions, const int64_t* slots, float scale_ub, const rrf_kv_cache* cache,
+    int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    rrf_status st;
+    if ((st = check_head_shape(tokens, q_heads, head_dim)) != RRF_OK) return st;
+    if ((st = check_head_shape(tokens, kv_heads, head_dim)) != RRF_OK) return st;
+    if ((st = check_scale_ub(scale_ub)) != RRF_OK) return st;
+    if ((st = check_norm(q_gamma, k_gamma, eps, weight_offset, cos_sin, max_positions, rot_dim,
+                         positions, head_dim, tokens == 0)) != RRF_OK || tokens == 0)
+        return st;
+    const Heads in[3] = {{q, q_token, q_head, q_heads}, {k, k_token, k_head, kv_heads},
+                         {v, v_token, v_head, kv_heads}};
+    const Heads out = {q_out, q_out_token, q_out_head, q_heads};
+    Region reads[8], writes[5];
+    int n = 0;
+    for (int i = 0; i < 3; ++i) {
+        if ((st = check_heads(in[i], tokens, head_dim, false)) != RRF_OK) return st;
+        if (i > 0 || !same(in[i], out, tokens))
+            reads[n++] = region_of(in[i].p, dims_of(in[i], tokens, head_dim), 2);
+    }
+    if ((st = check_heads(out, tokens, head_dim, true)) != RRF_OK) return st;
+    CacheDims d;
+    if ((st = check_cache(cache, kv_heads, head_dim, true, &d)) != RRF_OK) return st;
+    if (slots == nullptr) return RRF_ERR_NULL;
+    if (!aligned(slots, 8)) return RRF_ERR_ALIGN;
+    reads[n++] = flat(slots, tokens * 8);
+    n += add_norm_regions(q_gamma, k_gamma, cos_sin, max_positions, rot_dim, positions, tokens,
+                          head_dim, reads + n);
+    writes[0] = region_of(q_out, dims_of(out, tokens, head_dim), 2);
+    add_cache_regions(cache, d, writes + 1);
+    return check_regions(writes, 5, reads, n);
+}
+
+extern "C" rrf_status rrf_qk_norm_rope_kv_cache_fp8(
+    const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+    int64_t k_head, const void* v, int64_t v_token, int64_t v_head, void* q_out,
+    int64_t q_out_token, int64_t q_out_head, const void* q_gamma, const void* k_gamma, float eps,
+    float weight_offset, const float* cos_sin, int64_t max_positions, int64_t rot_dim,
+    int interleaved, const int64_t* positions, const int64_t* slots, float scale_ub,
+    const rrf_kv_cache* cache, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+    int64_t head_dim, rrf_stream_t stream) {
+    const rrf_status st = rrf_check_qk_norm_rope_kv_cache_args(
+        q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, q_out, q_out_token,
+        q_out_head, q_gamma, k_gamma, eps, weight_offset, cos_sin, max_positions, rot_dim,
+        positions, slots, scale_ub, cache, tokens, q_heads, kv_heads, head_dim);
+    if (st != RRF_OK || tokens == 0) return st;
+    HeadsArgs a = {};
+    a.q = view_of({q, q_token, q_head, q_heads});
+    a.k = view_of({k, k_token, k_head, kv_heads});
+    a.v = view_of({v, v_token, v_head, kv_heads});
+    a.q_out = view_of({q_out, q_out_token, q_out_head, q_heads});
+    a.slots = slots;
+    a.scale_ub = scale_ub;
+    set_norm(&a, q_gamma, k_gamma, eps, weight_offset, cos_sin, max_positions, rot_dim,
+             interleaved, positions, tokens, head_dim);
+    set_cache(&a, cache, kv_heads, head_dim);
+    a.num_slots = cache->num_pages * cache->page_size;
+    return run_heads(a, true, stream);
+}
+
+extern "C" rrf_status rrf_check_kv_cache_read_args(const rrf_kv_cache* cache,
+                                                   const int32_t* block_table,
+                                                   int64_t table_stride, int64_t table_width,
+                                                   const int32_t* seq_starts, int64_t sequences,
+                                                   const void* k_out, const void* v_out,
+                                                   int64_t rows, int64_t kv_heads,
+                                                   int64_t head_dim) {
+    rrf_status st;
+    if ((st = check_head_shape(rows, kv_heads, head_dim)) != RRF_OK) return st;
+    if (sequences < 0 || sequences > INT32_MAX / 2 || table_width < 0 ||
+        table_width > INT32_MAX / 2)
+        return RRF_ERR_SHAPE;
+    if (rows == 0 || sequences == 0) return RRF_OK;
+    const Dims table = {1, {sequences, 0, 0}, {table_stride, 0, 0}, table_width};
+    if (table_width > 0 && extent(table) == 0) return RRF_ERR_SHAPE;
+    CacheDims d;
+    if ((st = check_cache(cache, kv_heads, head_dim, false, &d)) != RRF_OK) return st;
+    if ((table_width > 0 && block_table == nullptr) || !seq_starts || !k_out || !v_out)
+        return RRF_ERR_NULL;
+    if (!aligned(block_table, 4) || !aligned(seq_starts, 4) || !aligned(k_out, 16) ||
+        !aligned(v_out, 16))
+        return RRF_ERR_ALIGN;
+    Region reads[6], writes[2];
+    int n = add_cache_regions(cache, d, reads);
+    reads[n++] = flat(seq_starts, (sequences + 1) * 4);
+    if (table_width > 0) reads[n++] = flat(block_table, extent(table) * 4);
+    const int64_t bytes = rows * kv_heads * head_dim * 2;
+    writes[0] = flat(k_out, bytes);
+    writes[1] = flat(v_out, bytes);
+    return check_regions(writes, 2, reads, n);
+}
+
+extern "C" rrf_status rrf_kv_cache_read_fp8(const rrf_kv_cache* cache,
+                                            const int32_t* block_table, int64_t table_stride,
+                                            int64_t table_width, const int32_t* seq_starts,
+                                            int64_t sequences, void* k_out, void* v_out,
+                                            int64_t rows, int64_t kv_heads, int64_t head_dim,
+                                            rrf_stream_t stream) {
+    rrf_status st = rrf_check_kv_cache_read_args(cache, block_table, table_stride, table_width,
+                                                 seq_starts, sequences, k_out, v_out, rows,
+                                                 kv_heads, head_dim);
+    if (st != RRF_OK || rows == 0 || sequences == 0) return st;
+    CacheReadArgs a = {};
+    set_cache(&a, cache, kv_heads, head_dim);
+    a.num_pages = cache->num_pages;
+    a.block_table = block_table;
+    a.table_stride = table_stride;
+    a.table_width = (int)table_width;
+    a.seq_starts = seq_starts;
+    a.sequences = (int)sequences;
+    a.heads = (int)kv_heads;
+    a.dim = (int)head_dim;
+    a.k_out = static_cast<uint16_t*>(k_out);
+    a.v_out = static_cast<uint16_t*>(v_out);
+    a.rows = (int)rows;
+    int sm_count = 0;
+    if ((st = current_sm_count(&sm_count)) != RRF_OK) return st;
+    if ((st = device_error_word(&a.err)) != RRF_OK) return st;
+    cudaError_t e;
+    if (!take_injected_failure(&e)) e = launch_cache_read(a, sm_count, (cudaStream_t)stream);
+    return e == cudaSuccess ? RRF_OK : cuda_fail(e);
+}
+
 extern "C" rrf_status rrf_plan_fused_ex(int num_inputs, int64_t rows, int64_t cols,
                                         int residual, int sm_count, int* cluster_size,
                                         int* block_threads, int* vecs_per_thread,

@@ -121,6 +121,67 @@ struct GemmArgs {
     int starve;            // test hook: the epilogue's extra wait runs out
 };
 
+// A [tokens, heads, head_dim] bf16 array (strides in elements; the head's
+// values are contiguous).
+struct HeadView {
+    uint16_t* p;
+    int64_t token_stride, head_stride;
+    int heads;
+};
+
+// The per-head pass over queries, keys and values (rrf_heads.cu).
+struct HeadsArgs {
+    HeadView q, k, v;      // v only with slots
+    HeadView q_out, k_out; // k_out only without slots
+    const uint4* q_gamma;  // [dim / 8]
+    const uint4* k_gamma;
+    const float* cos_sin;  // [max_positions, rot]: rot / 2 cosines, rot / 2 sines
+    const int64_t* positions;  // [tokens]
+    int64_t max_positions;
+    const int64_t* slots;  // [tokens], or null: nothing goes to a cache
+    uint8_t* k_codes;      // the cache: strides shared by keys and values
+    uint8_t* v_codes;
+    float* k_scales;
+    float* v_scales;
+    int64_t num_slots;
+    int64_t code_page, code_slot, code_head;
+    int64_t scale_page, scale_slot, scale_head;
+    int64_t code_end, scale_end;  // extents (the bounds-checking build's limits)
+    int page_size;
+    int tokens;
+    int dim, rot;
+    int interleaved;
+    float inv_dim;         // 1 / dim rounded to fp32
+    float eps, weight_offset, scale_ub;
+    unsigned int* err;
+    // set by the launcher: where the kinds of chunks begin, chunks and warps
+    // of a token
+    int key_chunk, value_chunk, chunks, warps_per_token;
+};
+
+// Reading a cache back (rrf_cache.cu).
+struct CacheReadArgs {
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
+    const float* k_scales;
+    const float* v_scales;
+    int64_t code_page, code_slot, code_head;
+    int64_t scale_page, scale_slot, scale_head;
+    int64_t code_end, scale_end;  // extents (the bounds-checking build's limits)
+    int64_t num_pages;
+    const int* block_table;   // [sequences, table_stride], table_width entries used
+    int64_t table_stride;
+    int table_width;
+    const int* seq_starts;    // [sequences + 1]
+    int sequences;
+    int page_size;
+    int heads, dim;
+    uint16_t* k_out;          // [rows, heads, dim]
+    uint16_t* v_out;
+    int rows;
+    unsigned int* err;
+};
+
 struct FusedLaunch {
     int cluster;          // blocks per row
     int threads;          // threads per block
@@ -163,6 +224,11 @@ cudaError_t launch_fused(const FusedArgs& a, int64_t rows, const FusedLaunch& l,
                          bool residual, cudaStream_t stream);
 
 cudaError_t launch_post(const PostArgs& a, int sm_count, bool pdl, cudaStream_t stream);
+
+// norm: q and k are normalised, rotated and written; else k and v go to the
+// cache as they are.
+cudaError_t launch_heads(const HeadsArgs& a, bool norm, int sm_count, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheReadArgs& a, int sm_count, cudaStream_t stream);
 
 cudaError_t launch_allreduce(const ArArgs& a, const ArLaunch& l, cudaStream_t stream);
 // The GEMM kernel a shape takes (pure host arithmetic; the launchers follow
