@@ -523,6 +523,43 @@ rrf_status rrf_check_scaled_mm_args(const void* a, const float* a_scale, const v
                                     const float* b_scale, const void* bias, const void* out,
                                     int64_t M, int64_t N, int64_t K);
 
+/* Activations of the products below (erf and tanh forms of gelu). */
+#define RRF_ACT_NONE 0
+#define RRF_ACT_RELU 1
+#define RRF_ACT_GELU 2      /* y (1 + erf(y / sqrt 2)) / 2                              */
+#define RRF_ACT_GELU_TANH 3 /* y (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) / 2        */
+#define RRF_ACT_SILU 4      /* y / (1 + exp(-y))                                        */
+
+/* rrf_scaled_mm_fp8_act, rrf_scaled_mm_mxfp8_act -- the two products with the
+ * rest of a layer's projection in their epilogue:
+ *   y         = the product, scaled, plus bias, as above but not rounded
+ *   out[m][n] = RN_bf16( act(y[m][n]) + residual[m][n] )
+ * all in fp32, rounded once.
+ * activation  one of RRF_ACT_*
+ * residual    bf16 [M, N] or NULL, 16-byte aligned; it may be out (the update
+ *             in place) but not overlap it otherwise
+ * The other arguments, the shapes and the kernels (rrf_plan_scaled_mm) are
+ * those of rrf_scaled_mm_fp8 and rrf_scaled_mm_mxfp8.
+ * Errors: as theirs, and RRF_ERR_VALUE (activation). */
+rrf_status rrf_scaled_mm_fp8_act(const void* a, const float* a_scale, const void* b,
+                                 const float* b_scale, const void* bias, int activation,
+                                 const void* residual, void* out, int64_t M, int64_t N, int64_t K,
+                                 rrf_stream_t stream);
+rrf_status rrf_scaled_mm_mxfp8_act(const void* a, const void* sa, const void* b, const void* sb,
+                                   const void* bias, int activation, const void* residual,
+                                   void* out, int64_t M, int64_t N, int64_t K,
+                                   rrf_stream_t stream);
+
+/* Their host validation alone (no GPU needed). */
+rrf_status rrf_check_scaled_mm_act_args(const void* a, const float* a_scale, const void* b,
+                                        const float* b_scale, const void* bias, int activation,
+                                        const void* residual, const void* out, int64_t M,
+                                        int64_t N, int64_t K);
+rrf_status rrf_check_scaled_mm_mx_act_args(const void* a, const void* sa, const void* b,
+                                           const void* sb, const void* bias, int activation,
+                                           const void* residual, const void* out, int64_t M,
+                                           int64_t N, int64_t K);
+
 /* GEMM kernels (rrf_plan_scaled_mm). */
 #define RRF_GEMM_KERNEL_PAIR 1 /* 256 x 256 tiles on SM pairs (two-CTA MMA)           */
 #define RRF_GEMM_KERNEL_TILE 2 /* one persistent CTA per SM walking 128 x tile_n output

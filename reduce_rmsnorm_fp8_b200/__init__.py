@@ -22,6 +22,8 @@ Functions, named after the C entry points:
   rrf_sum_rmsnorm_fp8_pre / rrf_rmsnorm_fp8_post: the two phases of the
       sharded form (a row's hidden dimension split across devices); the
       torch.distributed glue between them is in ``sharded.py``
+  rrf_scaled_mm_fp8_act, rrf_scaled_mm_mxfp8_act: the FP8 products with
+      bias, activation and residual in their epilogue
   rrf_qk_norm_rope, rrf_kv_cache_write_fp8, rrf_qk_norm_rope_kv_cache_fp8,
       rrf_kv_cache_read_fp8: the per-head norm and rotation of queries and
       keys (rope_table makes its table), and a paged FP8 cache of keys and
@@ -49,7 +51,8 @@ _EXPORTS = (
     "RRF_GEMM_KERNEL_SWAP", "RRF_FLAG_NO_PREFETCH", "RRF_FLAG_PREFETCH", "rrf_plan_fused_ex",
     "RRF_DEVICE_ERROR_BOUNDS", "RRF_DEVICE_ERROR_INDEX", "RRF_MAX_HEAD_DIM", "RrfKvCache",
     "rope_table", "rrf_qk_norm_rope", "rrf_kv_cache_write_fp8", "rrf_kv_cache_read_fp8",
-    "rrf_qk_norm_rope_kv_cache_fp8",
+    "rrf_qk_norm_rope_kv_cache_fp8", "rrf_scaled_mm_fp8_act", "rrf_scaled_mm_mxfp8_act",
+    "RRF_ACT_NONE", "RRF_ACT_RELU", "RRF_ACT_GELU", "RRF_ACT_GELU_TANH", "RRF_ACT_SILU",
 )
 
 __all__ = list(_EXPORTS)

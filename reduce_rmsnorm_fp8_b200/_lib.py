@@ -37,6 +37,11 @@ RRF_MAX_HEAD_DIM = 512
 RRF_GEMM_KERNEL_PAIR = 1
 RRF_GEMM_KERNEL_TILE = 2
 RRF_GEMM_KERNEL_SWAP = 3
+RRF_ACT_NONE = 0
+RRF_ACT_RELU = 1
+RRF_ACT_GELU = 2
+RRF_ACT_GELU_TANH = 3
+RRF_ACT_SILU = 4
 
 
 class Status(enum.IntEnum):
@@ -813,3 +818,72 @@ def rrf_kv_cache_read_fp8(k_cache, k_scales, v_cache, v_scales, block_table, seq
             _vector(seq_starts, "seq_starts", torch.int32, sequences + 1, index), sequences,
             k_out.data_ptr(), v_out.data_ptr(), rows, heads, dim)
     return k_out, v_out
+
+
+# ------------------------------------------- products with their epilogue ---
+
+_mm_act_args = [_vp] * 5 + [_int, _vp, _vp] + [_i64] * 3
+for _name in ("rrf_scaled_mm_fp8_act", "rrf_scaled_mm_mxfp8_act"):
+    getattr(lib, _name).restype = _int
+    getattr(lib, _name).argtypes = _mm_act_args + [_vp]
+for _name in ("rrf_check_scaled_mm_act_args", "rrf_check_scaled_mm_mx_act_args"):
+    getattr(lib, _name).restype = _int
+    getattr(lib, _name).argtypes = _mm_act_args
+
+_ACTIVATIONS = {None: RRF_ACT_NONE, "none": RRF_ACT_NONE, "relu": RRF_ACT_RELU,
+                "gelu": RRF_ACT_GELU, "gelu_tanh": RRF_ACT_GELU_TANH, "silu": RRF_ACT_SILU}
+
+
+def _mm_operands(a, b, bias, activation, residual, out):
+    """(index, M, N, K, activation code, out) of a checked product."""
+    torch = _torch()
+    index = a.get_device()
+    f8 = torch.float8_e4m3fn
+    if a.dtype is not f8 or b.dtype is not f8 or a.dim() != 2 or b.dim() != 2 or index < 0 or \
+            b.get_device() != index or not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a and b must be contiguous 2-D float8_e4m3fn tensors on one CUDA device")
+    (m, k), (n, kb) = a.shape, b.shape
+    if kb != k:
+        raise ValueError("a and b need the same K")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(filter(None, _ACTIVATIONS))}")
+    bf16 = torch.bfloat16
+    if bias is not None:
+        _vector(bias, "bias", bf16, n, index)
+    for x, name in ((residual, "residual"), (out, "out")):
+        if x is not None and (x.dtype is not bf16 or x.shape != (m, n) or
+                              x.get_device() != index or not x.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bf16 [{m}, {n}] tensor on a's device")
+    if out is None:
+        out = torch.empty((m, n), dtype=bf16, device=a.device)
+    return index, m, n, k, _ACTIVATIONS[activation], out
+
+
+def rrf_scaled_mm_fp8_act(a, a_scale, b, b_scale, bias=None, activation="none", residual=None,
+                          out=None):
+    """out = RN_bf16(act((a @ b^T) * a_scale * b_scale + bias) + residual):
+    rrf_scaled_mm_fp8 with the rest of a projection in its epilogue, rounded
+    once.  activation: "none", "relu", "gelu" (erf), "gelu_tanh" or "silu";
+    residual: bf16 [M, N] or None; pass it as out too for an update in place.
+    Returns out, bf16 [M, N]."""
+    index, m, n, k, act, out = _mm_operands(a, b, bias, activation, residual, out)
+    f32 = _torch().float32
+    _launch(index, lib.rrf_scaled_mm_fp8_act, a.data_ptr(),
+            _vector(a_scale, "a_scale", f32, m, index), b.data_ptr(),
+            _vector(b_scale, "b_scale", f32, n, index),
+            None if bias is None else bias.data_ptr(), act,
+            None if residual is None else residual.data_ptr(), out.data_ptr(), m, n, k)
+    return out
+
+
+def rrf_scaled_mm_mxfp8_act(a, sa, b, sb, bias=None, activation="none", residual=None, out=None):
+    """rrf_scaled_mm_mxfp8 with the epilogue of rrf_scaled_mm_fp8_act: sa and
+    sb are E8M0 scale codes in the blocked order.  Returns out, bf16 [M, N]."""
+    index, m, n, k, act, out = _mm_operands(a, b, bias, activation, residual, out)
+    u8 = _torch().uint8
+    _launch(index, lib.rrf_scaled_mm_mxfp8_act, a.data_ptr(),
+            _vector(sa, "sa", u8, mx_blocked_bytes(m, k), index), b.data_ptr(),
+            _vector(sb, "sb", u8, mx_blocked_bytes(n, k), index),
+            None if bias is None else bias.data_ptr(), act,
+            None if residual is None else residual.data_ptr(), out.data_ptr(), m, n, k)
+    return out

@@ -922,10 +922,35 @@ extern "C" rrf_status rrf_check_scaled_mm_args(const void* a, const float* a_sca
     return RRF_OK;
 }
 
-extern "C" rrf_status rrf_scaled_mm_fp8(const void* a, const float* a_scale, const void* b,
-                                        const float* b_scale, const void* bias, void* out,
-                                        int64_t M, int64_t N, int64_t K, rrf_stream_t stream) {
-    rrf_status st = rrf_check_scaled_mm_args(a, a_scale, b, b_scale, bias, out, M, N, K);
+// The epilogue arguments beside a checked product's: the activation, and a
+// residual that is out itself or does not overlap it.
+static rrf_status check_epilogue(int activation, const void* residual, const void* out, int64_t M,
+                                 int64_t N) {
+    if (activation < RRF_ACT_NONE || activation > RRF_ACT_SILU) return RRF_ERR_VALUE;
+    if (M == 0 || residual == nullptr) return RRF_OK;
+    if (!aligned(residual, 16)) return RRF_ERR_ALIGN;
+    const int64_t bytes = M * N * 2;
+    return residual != out && overlap(range_of(residual, bytes), range_of(out, bytes))
+               ? RRF_ERR_ALIAS
+               : RRF_OK;
+}
+
+extern "C" rrf_status rrf_check_scaled_mm_act_args(const void* a, const float* a_scale,
+                                                   const void* b, const float* b_scale,
+                                                   const void* bias, int activation,
+                                                   const void* residual, const void* out,
+                                                   int64_t M, int64_t N, int64_t K) {
+    const rrf_status st = rrf_check_scaled_mm_args(a, a_scale, b, b_scale, bias, out, M, N, K);
+    return st != RRF_OK ? st : check_epilogue(activation, residual, out, M, N);
+}
+
+extern "C" rrf_status rrf_scaled_mm_fp8_act(const void* a, const float* a_scale, const void* b,
+                                            const float* b_scale, const void* bias,
+                                            int activation, const void* residual, void* out,
+                                            int64_t M, int64_t N, int64_t K,
+                                            rrf_stream_t stream) {
+    rrf_status st = rrf_check_scaled_mm_act_args(a, a_scale, b, b_scale, bias, activation,
+                                                 residual, out, M, N, K);
     if (st != RRF_OK || M == 0) return st;
     int sm_count = 0;
     if ((st = current_sm_count(&sm_count)) != RRF_OK) return st;
@@ -941,9 +966,18 @@ extern "C" rrf_status rrf_scaled_mm_fp8(const void* a, const float* a_scale, con
     g.K = (int)K;
     g.err = err;
     g.starve = take_starve_gemm();
+    g.act = activation;
+    g.residual = static_cast<const uint16_t*>(residual);
     cudaError_t e;
     if (!take_injected_failure(&e)) e = launch_scaled_mm(g, a, b, sm_count, (cudaStream_t)stream);
     return e == cudaSuccess ? RRF_OK : cuda_fail(e);
+}
+
+extern "C" rrf_status rrf_scaled_mm_fp8(const void* a, const float* a_scale, const void* b,
+                                        const float* b_scale, const void* bias, void* out,
+                                        int64_t M, int64_t N, int64_t K, rrf_stream_t stream) {
+    return rrf_scaled_mm_fp8_act(a, a_scale, b, b_scale, bias, RRF_ACT_NONE, nullptr, out, M, N,
+                                 K, stream);
 }
 
 extern "C" rrf_status rrf_plan_scaled_mm(int64_t M, int64_t N, int64_t K, int mx, int sm_count,
@@ -996,10 +1030,21 @@ extern "C" rrf_status rrf_check_scaled_mm_mx_args(const void* a, const void* sa,
     return RRF_OK;
 }
 
-extern "C" rrf_status rrf_scaled_mm_mxfp8(const void* a, const void* sa, const void* b,
-                                          const void* sb, const void* bias, void* out, int64_t M,
-                                          int64_t N, int64_t K, rrf_stream_t stream) {
-    rrf_status st = rrf_check_scaled_mm_mx_args(a, sa, b, sb, bias, out, M, N, K);
+extern "C" rrf_status rrf_check_scaled_mm_mx_act_args(const void* a, const void* sa,
+                                                      const void* b, const void* sb,
+                                                      const void* bias, int activation,
+                                                      const void* residual, const void* out,
+                                                      int64_t M, int64_t N, int64_t K) {
+    const rrf_status st = rrf_check_scaled_mm_mx_args(a, sa, b, sb, bias, out, M, N, K);
+    return st != RRF_OK ? st : check_epilogue(activation, residual, out, M, N);
+}
+
+extern "C" rrf_status rrf_scaled_mm_mxfp8_act(const void* a, const void* sa, const void* b,
+                                              const void* sb, const void* bias, int activation,
+                                              const void* residual, void* out, int64_t M,
+                                              int64_t N, int64_t K, rrf_stream_t stream) {
+    rrf_status st = rrf_check_scaled_mm_mx_act_args(a, sa, b, sb, bias, activation, residual, out,
+                                                    M, N, K);
     if (st != RRF_OK || M == 0) return st;
     int sm_count = 0;
     if ((st = current_sm_count(&sm_count)) != RRF_OK) return st;
@@ -1013,11 +1058,20 @@ extern "C" rrf_status rrf_scaled_mm_mxfp8(const void* a, const void* sa, const v
     g.K = (int)K;
     g.err = err;
     g.starve = take_starve_gemm();
+    g.act = activation;
+    g.residual = static_cast<const uint16_t*>(residual);
     cudaError_t e;
     if (!take_injected_failure(&e))
         e = launch_scaled_mm_mx(g, a, b, static_cast<const uint8_t*>(sa),
                                 static_cast<const uint8_t*>(sb), sm_count, (cudaStream_t)stream);
     return e == cudaSuccess ? RRF_OK : cuda_fail(e);
+}
+
+extern "C" rrf_status rrf_scaled_mm_mxfp8(const void* a, const void* sa, const void* b,
+                                          const void* sb, const void* bias, void* out, int64_t M,
+                                          int64_t N, int64_t K, rrf_stream_t stream) {
+    return rrf_scaled_mm_mxfp8_act(a, sa, b, sb, bias, RRF_ACT_NONE, nullptr, out, M, N, K,
+                                   stream);
 }
 
 // ------------------------------------------- heads and the FP8 cache ---

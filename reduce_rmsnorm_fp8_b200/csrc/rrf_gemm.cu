@@ -182,27 +182,118 @@ __host__ __device__ constexpr uint32_t f8_idesc(int bn) {
 
 // ------------------------------------------------------------------ kernel --
 
+// The full epilogue (EPI kernels): out = RN_bf16(act(y) + residual), y the
+// scaled sum with its bias, all in fp32.  The activations, with the hardware's
+// exponential and quotient (a few ulp; the result is rounded to bf16, 2^16
+// times coarser):
+//   silu       y / (1 + e^-y)
+//   gelu       y erfc(-y / sqrt 2) / 2 (not 1 + erf, which cancels below 0)
+//   gelu_tanh  y (1 + tanh u) / 2 = y / (1 + e^-2u), u = sqrt(2 / pi)
+//              (y + 0.044715 y^3)
+
+// y / (1 + 2^t).  Both sides of the quotient are 2^-8 times that: the
+// approximate quotient is 0 for a divisor above 2^126, and so only where the
+// result is below 2^-126.
+__device__ __forceinline__ float over_one_plus_exp2(float y, float t) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t - 8.0f));
+    return __fdividef(y * 0.00390625f, 0.00390625f + e);
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float y) {
+    constexpr float kLog2e = 1.44269504f;
+    if constexpr (ACT == RRF_ACT_RELU) return y < 0.0f ? 0.0f : y;  // (a NaN stays one)
+    if constexpr (ACT == RRF_ACT_SILU) return over_one_plus_exp2(y, -kLog2e * y);
+    if constexpr (ACT == RRF_ACT_GELU) return 0.5f * y * erfcf(-0.70710678f * y);
+    if constexpr (ACT == RRF_ACT_GELU_TANH)
+        return over_one_plus_exp2(y, -1.5957691f * kLog2e * (y + 0.044715f * y * y * y));
+    return y;
+}
+
+template <int N>
+__device__ __forceinline__ void activate_all(int act, float y[N]) {
+    if (act == RRF_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = activate<RRF_ACT_RELU>(y[i]);
+    } else if (act == RRF_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = activate<RRF_ACT_SILU>(y[i]);
+    } else if (act == RRF_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = activate<RRF_ACT_GELU>(y[i]);
+    } else if (act == RRF_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = activate<RRF_ACT_GELU_TANH>(y[i]);
+    }
+}
+
+// 16 bytes of a residual, which may be the output itself: a coherent load that
+// stays where it is written (behind the wait for the previous kernel).
+__device__ __forceinline__ uint4 ld_residual(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // The epilogue of 32 accumulator columns [n, n + 32) of one output row: both
 // scales and the bias in fp32, one rounding to bf16, 64-byte stores (16 or
 // 32 columns valid: N % 16 == 0).
+template <bool EPI>
 __device__ __forceinline__ void store_row_chunk(const GemmArgs& g, const float v[32], float sa,
                                                 int row, int n) {
     if (!RRF_IN_BOUNDS(row >= 0 && row < g.M && n >= 0 && n < g.N, g.err)) return;
     const int valid = g.N - n < 32 ? g.N - n : 32;
     uint32_t packed[16];
+    if constexpr (EPI) {
+        uint4 res[4];
+        const uint4* src = reinterpret_cast<const uint4*>(g.residual + (int64_t)row * g.N + n);
+        if (g.residual != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        // (the MX GEMM has no column scales: its scales act inside the MMA)
-        const float s0 = i < valid ? (g.b_scale != nullptr ? g.b_scale[n + i] : 1.0f) : 0.0f;
-        const float s1 =
-            i + 1 < valid ? (g.b_scale != nullptr ? g.b_scale[n + i + 1] : 1.0f) : 0.0f;
-        float y0 = __fmul_rn(__fmul_rn(v[i], sa), s0);
-        float y1 = __fmul_rn(__fmul_rn(v[i + 1], sa), s1);
-        if (g.bias != nullptr && i < valid) {
-            y0 = __fadd_rn(y0, __uint_as_float((uint32_t)g.bias[n + i] << 16));
-            y1 = __fadd_rn(y1, __uint_as_float((uint32_t)g.bias[n + i + 1] << 16));
+            for (int q = 0; q < 4; ++q)
+                if (q * 8 < valid) res[q] = ld_residual(src + q);
         }
-        packed[i / 2] = f32x2_to_bf16x2(y0, y1);
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            y[i] = v[i];
+            if (g.b_scale != nullptr && i < valid)
+                y[i] = __fmul_rn(__fmul_rn(v[i], sa), g.b_scale[n + i]);
+            if (g.bias != nullptr && i < valid)
+                y[i] = __fadd_rn(y[i], __uint_as_float((uint32_t)g.bias[n + i] << 16));
+        }
+        activate_all<32>(g.act, y);
+        if (g.residual != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q * 8 < valid) {
+                    float r[8];
+                    bf16x8_to_f32(res[q], r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[8 * q + i] = __fadd_rn(y[8 * q + i], r[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) packed[i / 2] = f32x2_to_bf16x2(y[i], y[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            // (the MX GEMM has no column scales: its scales act inside the MMA)
+            const float s0 = i < valid ? (g.b_scale != nullptr ? g.b_scale[n + i] : 1.0f) : 0.0f;
+            const float s1 =
+                i + 1 < valid ? (g.b_scale != nullptr ? g.b_scale[n + i + 1] : 1.0f) : 0.0f;
+            float y0 = __fmul_rn(__fmul_rn(v[i], sa), s0);
+            float y1 = __fmul_rn(__fmul_rn(v[i + 1], sa), s1);
+            if (g.bias != nullptr && i < valid) {
+                y0 = __fadd_rn(y0, __uint_as_float((uint32_t)g.bias[n + i] << 16));
+                y1 = __fadd_rn(y1, __uint_as_float((uint32_t)g.bias[n + i + 1] << 16));
+            }
+            packed[i / 2] = f32x2_to_bf16x2(y0, y1);
+        }
     }
     uint4* dst = reinterpret_cast<uint4*>(g.out + (int64_t)row * g.N + n);
 #pragma unroll
@@ -280,7 +371,7 @@ __device__ __forceinline__ void load_group(uint8_t* dst, const CUtensorMap* ma,
 // the 128 x BN tiles, so the CTAs working at one time share A rows and B
 // columns in L2).  The accumulator is double-buffered in tensor memory: the
 // MMAs of a CTA's next tile run while the epilogue warps drain this one.
-template <int BN, int AROWS, int Z>
+template <int BN, int AROWS, int Z, bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     scaled_mm_kernel(const __grid_constant__ CUtensorMap tma_a,
                      const __grid_constant__ CUtensorMap tma_b, const GemmArgs g) {
@@ -412,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_load_32(base + (uint32_t)c, v);
                 const int n = n0 + c;
                 if (row >= g.M || n >= g.N) continue;
-                store_row_chunk(g, v, sa, row, n);
+                store_row_chunk<EPI>(g, v, sa, row, n);
             }
             // this warp's reads of the accumulator are done: hand it back
             tc_fence_before_sync();
@@ -555,6 +646,11 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// A bf16 value of memory the kernel may also write (a residual in place).
+__device__ __forceinline__ float bf16_at(const uint16_t* p) {
+    return __uint_as_float((uint32_t)*reinterpret_cast<const volatile uint16_t*>(p) << 16);
+}
+
 // NA consecutive fp32 accumulator columns of this thread's lane (NA = 8, 16
 // or 32).
 template <int NA>
@@ -587,7 +683,7 @@ __device__ __forceinline__ void tmem_load_cols(uint32_t taddr, float v[NA]) {
 
 // sfx, sfw: the MX form's scale codes of the call's rows and of the weight
 // (the blocked order); null in the per-token form.
-template <int NA, int Z, bool MX>
+template <int NA, int Z, bool MX, bool EPI>
 __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
     scaled_mm_swap_pairk_kernel(const __grid_constant__ CUtensorMap tma_x,
                                 const __grid_constant__ CUtensorMap tma_w, const GemmArgs g,
@@ -846,12 +942,33 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
                     const float sb = MX ? 1.0f : g.b_scale[n];
                     const float bias =
                         g.bias != nullptr ? __uint_as_float((uint32_t)g.bias[n] << 16) : 0.0f;
+                    if constexpr (EPI) {
+                        // NA values at once, so that the activation's branch
+                        // is taken once
+#pragma unroll
+                        for (int m = 0; m < NA; ++m) {
+                            o[m] = __fadd_rn(v[m], o[m]);
+                            if constexpr (!MX)
+                                if (m < g.M)
+                                    o[m] = __fmul_rn(__fmul_rn(o[m], __ldg(g.a_scale + m)), sb);
+                            if (g.bias != nullptr) o[m] = __fadd_rn(o[m], bias);
+                        }
+                        activate_all<NA>(g.act, o);
+                    }
 #pragma unroll
                     for (int m = 0; m < NA; ++m) {
                         if (m < g.M) {
-                            float y = __fadd_rn(v[m], o[m]);
-                            if constexpr (!MX) y = __fmul_rn(__fmul_rn(y, __ldg(g.a_scale + m)), sb);
-                            if (g.bias != nullptr) y = __fadd_rn(y, bias);
+                            float y;
+                            if constexpr (EPI) {
+                                y = o[m];
+                                if (g.residual != nullptr)
+                                    y = __fadd_rn(y, bf16_at(g.residual + (int64_t)m * g.N + n));
+                            } else {
+                                y = __fadd_rn(v[m], o[m]);
+                                if constexpr (!MX)
+                                    y = __fmul_rn(__fmul_rn(y, __ldg(g.a_scale + m)), sb);
+                                if (g.bias != nullptr) y = __fadd_rn(y, bias);
+                            }
                             g.out[(int64_t)m * g.N + n] =
                                 (uint16_t)(f32x2_to_bf16x2(y, 0.0f) & 0xFFFFu);
                         }
@@ -968,6 +1085,7 @@ struct PairTile {
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarriers * 8 + 16;
 };
 
+template <bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     scaled_mm_pair_kernel(const __grid_constant__ CUtensorMap tma_a,
                           const __grid_constant__ CUtensorMap tma_b, const GemmArgs g) {
@@ -1106,7 +1224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_load_32(base + (uint32_t)c, v);
                 const int n = n0 + c;
                 if (row >= g.M || n >= g.N) continue;
-                store_row_chunk(g, v, sa, row, n);
+                store_row_chunk<EPI>(g, v, sa, row, n);
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -1166,7 +1284,7 @@ struct MxTile {
     static_assert(kSmemBytes <= 227 * 1024, "stages exceed the shared memory of a CTA");
 };
 
-template <int BN, int AROWS, int Z>
+template <int BN, int AROWS, int Z, bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     scaled_mm_mx_kernel(const __grid_constant__ CUtensorMap tma_a,
                         const __grid_constant__ CUtensorMap tma_b, const GemmArgs g,
@@ -1312,7 +1430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_load_32(base + (uint32_t)c, v);
                 const int n = n0 + c;
                 if (row >= g.M || n >= g.N) continue;
-                store_row_chunk(g, v, 1.0f, row, n);  // g.b_scale is null: no scaling
+                store_row_chunk<EPI>(g, v, 1.0f, row, n);  // g.b_scale is null: no scaling
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -1402,6 +1520,7 @@ struct MxPairTile {
 static_assert(MxPairTile::kSfbCol + 8 <= MxPairTile::kTmemCols, "scale columns past the allocation");
 static_assert(MxPairTile::kSmemBytes <= 227 * 1024, "stages exceed the shared memory of a CTA");
 
+template <bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     scaled_mm_mx_pair_kernel(const __grid_constant__ CUtensorMap tma_a,
                              const __grid_constant__ CUtensorMap tma_b,
@@ -1560,7 +1679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int n = n0 + c;
                 if (row >= g.M || n >= g.N) continue;
-                store_row_chunk(g, v, 1.0f, row, n);  // g.b_scale is null: no scaling
+                store_row_chunk<EPI>(g, v, 1.0f, row, n);  // g.b_scale is null: no scaling
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -1720,13 +1839,13 @@ bool make_maps(CUtensorMap* ma, CUtensorMap* mb, const GemmArgs& g, const void* 
     return make_map3(ma, a, g.M, g.K, arows, z) && make_map3(mb, b, g.N, g.K, brows, z);
 }
 
-template <int BN, int AROWS, int Z>
+template <int BN, int AROWS, int Z, bool EPI>
 cudaError_t launch_bn(const GemmArgs& g, const void* a, const void* b, int sm_count,
                       cudaStream_t stream) {
     using T = Tile<BN, AROWS, Z>;
     CUtensorMap ma, mb;
     if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z)) return cudaErrorInvalidValue;
-    constexpr auto kernel = scaled_mm_kernel<BN, AROWS, Z>;
+    constexpr auto kernel = scaled_mm_kernel<BN, AROWS, Z, EPI>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + BN - 1) / BN) * ((g.M + kBM - 1) / kBM);
@@ -1736,7 +1855,7 @@ cudaError_t launch_bn(const GemmArgs& g, const void* a, const void* b, int sm_co
 
 // sfa, sfb: the MX form's scale codes of a and b (the blocked order), else
 // null.
-template <int NA, int Z, bool MX = false>
+template <int NA, int Z, bool MX, bool EPI>
 cudaError_t launch_swap_pairk(const GemmArgs& g, const void* a, const void* b, int sm_count,
                               cudaStream_t stream, const uint8_t* sfa = nullptr,
                               const uint8_t* sfb = nullptr) {
@@ -1744,7 +1863,7 @@ cudaError_t launch_swap_pairk(const GemmArgs& g, const void* a, const void* b, i
     CUtensorMap mx, mw;
     if (!make_map3(&mx, a, g.M, g.K, NA, Z) || !make_map3(&mw, b, g.N, g.K, T::kWRows, Z))
         return cudaErrorInvalidValue;
-    constexpr auto kernel = scaled_mm_swap_pairk_kernel<NA, Z, MX>;
+    constexpr auto kernel = scaled_mm_swap_pairk_kernel<NA, Z, MX, EPI>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (g.N + T::kWRows - 1) / T::kWRows;
@@ -1753,26 +1872,27 @@ cudaError_t launch_swap_pairk(const GemmArgs& g, const void* a, const void* b, i
                                      mw, g, sfa, sfb);
 }
 
+template <bool EPI>
 cudaError_t launch_pair(const GemmArgs& g, const void* a, const void* b, int sm_count,
                         cudaStream_t stream) {
     using T = PairTile;
     CUtensorMap ma, mb;
     if (!make_map(&ma, a, g.M, g.K, 128) || !make_map(&mb, b, g.N, g.K, 128))
         return cudaErrorInvalidValue;
-    const cudaError_t e = enable_dynamic_smem<scaled_mm_pair_kernel>(T::kSmemBytes);
+    const cudaError_t e = enable_dynamic_smem<scaled_mm_pair_kernel<EPI>>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + 255) / 256) * ((g.M + 255) / 256);
     const int64_t pairs = tiles < sm_count / 2 ? tiles : sm_count / 2;
-    return launch_on_pairs(scaled_mm_pair_kernel, pairs, T::kSmemBytes, stream, ma, mb, g);
+    return launch_on_pairs(scaled_mm_pair_kernel<EPI>, pairs, T::kSmemBytes, stream, ma, mb, g);
 }
 
-template <int BN, int AROWS, int Z>
+template <int BN, int AROWS, int Z, bool EPI>
 cudaError_t launch_mx(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
                       const uint8_t* sfb, int sm_count, cudaStream_t stream) {
     using T = MxTile<BN, AROWS, Z>;
     CUtensorMap ma, mb;
     if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z)) return cudaErrorInvalidValue;
-    constexpr auto kernel = scaled_mm_mx_kernel<BN, AROWS, Z>;
+    constexpr auto kernel = scaled_mm_mx_kernel<BN, AROWS, Z, EPI>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + BN - 1) / BN) * ((g.M + kBM - 1) / kBM);
@@ -1780,6 +1900,7 @@ cudaError_t launch_mx(const GemmArgs& g, const void* a, const void* b, const uin
     return launch_persistent(kernel, grid, T::kSmemBytes, stream, ma, mb, g, sfa, sfb);
 }
 
+template <bool EPI>
 cudaError_t launch_mx_pair(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
                            const uint8_t* sfb, int sm_count, cudaStream_t stream) {
     using T = MxPairTile;
@@ -1787,12 +1908,12 @@ cudaError_t launch_mx_pair(const GemmArgs& g, const void* a, const void* b, cons
     if (!make_map(&ma, a, g.M, g.K, 128) || !make_map(&mb, b, g.N, g.K, 128) ||
         !make_sf_map(&msa, sfa, g.M, g.K, 1) || !make_sf_map(&msb, sfb, g.N, g.K, 2))
         return cudaErrorInvalidValue;
-    const cudaError_t e = enable_dynamic_smem<scaled_mm_mx_pair_kernel>(T::kSmemBytes);
+    const cudaError_t e = enable_dynamic_smem<scaled_mm_mx_pair_kernel<EPI>>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + 255) / 256) * ((g.M + 255) / 256);
     const int64_t pairs = tiles < sm_count / 2 ? tiles : sm_count / 2;
-    return launch_on_pairs(scaled_mm_mx_pair_kernel, pairs, T::kSmemBytes, stream, ma, mb, msa,
-                           msb, g);
+    return launch_on_pairs(scaled_mm_mx_pair_kernel<EPI>, pairs, T::kSmemBytes, stream, ma, mb,
+                           msa, msb, g);
 }
 
 }  // namespace
@@ -1852,37 +1973,59 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
     return tile(kGemmTile, kBM, 64, atoms ? 2 : 1);
 }
 
+namespace {
+
+template <bool EPI>
+cudaError_t dispatch_mx(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
+                        const uint8_t* sfb, int sm_count, cudaStream_t stream) {
+    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, true, sm_count);
+    if (p.kernel == kGemmPair) return launch_mx_pair<EPI>(g, a, b, sfa, sfb, sm_count, stream);
+    if (p.kernel == kGemmSwap) {
+        if (p.a_rows == 8)
+            return launch_swap_pairk<8, 4, true, EPI>(g, a, b, sm_count, stream, sfa, sfb);
+        if (p.a_rows == 16)
+            return launch_swap_pairk<16, 4, true, EPI>(g, a, b, sm_count, stream, sfa, sfb);
+        return launch_swap_pairk<32, 4, true, EPI>(g, a, b, sm_count, stream, sfa, sfb);
+    }
+    if (p.tile_n == 128) return launch_mx<128, kBM, 1, EPI>(g, a, b, sfa, sfb, sm_count, stream);
+    if (p.a_rows == 64) return launch_mx<64, 64, 4, EPI>(g, a, b, sfa, sfb, sm_count, stream);
+    return launch_mx<64, kBM, 2, EPI>(g, a, b, sfa, sfb, sm_count, stream);
+}
+
+template <bool EPI>
+cudaError_t dispatch(const GemmArgs& g, const void* a, const void* b, int sm_count,
+                     cudaStream_t stream) {
+    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, false, sm_count);
+    if (p.kernel == kGemmPair) return launch_pair<EPI>(g, a, b, sm_count, stream);
+    if (p.kernel == kGemmSwap) {
+        if (p.a_rows == 8) return launch_swap_pairk<8, 8, false, EPI>(g, a, b, sm_count, stream);
+        if (p.a_rows == 16) return launch_swap_pairk<16, 4, false, EPI>(g, a, b, sm_count, stream);
+        return launch_swap_pairk<32, 4, false, EPI>(g, a, b, sm_count, stream);
+    }
+    if (p.tile_n == 128) return launch_bn<128, kBM, 1, EPI>(g, a, b, sm_count, stream);
+    if (p.a_rows == 64)
+        return p.k_tiles_per_stage == 4 ? launch_bn<64, 64, 4, EPI>(g, a, b, sm_count, stream)
+                                        : launch_bn<64, 64, 1, EPI>(g, a, b, sm_count, stream);
+    return p.k_tiles_per_stage == 2 ? launch_bn<64, kBM, 2, EPI>(g, a, b, sm_count, stream)
+                                    : launch_bn<64, kBM, 1, EPI>(g, a, b, sm_count, stream);
+}
+
+}  // namespace
+
+// A call with neither activation nor residual is the plain product.
 cudaError_t launch_scaled_mm_mx(const GemmArgs& g, const void* a, const void* b,
                                 const uint8_t* sfa, const uint8_t* sfb, int sm_count,
                                 cudaStream_t stream) {
-    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, true, sm_count);
-    if (p.kernel == kGemmPair) return launch_mx_pair(g, a, b, sfa, sfb, sm_count, stream);
-    if (p.kernel == kGemmSwap) {
-        if (p.a_rows == 8) return launch_swap_pairk<8, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
-        if (p.a_rows == 16)
-            return launch_swap_pairk<16, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
-        return launch_swap_pairk<32, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
-    }
-    if (p.tile_n == 128) return launch_mx<128, kBM, 1>(g, a, b, sfa, sfb, sm_count, stream);
-    if (p.a_rows == 64) return launch_mx<64, 64, 4>(g, a, b, sfa, sfb, sm_count, stream);
-    return launch_mx<64, kBM, 2>(g, a, b, sfa, sfb, sm_count, stream);
+    return g.act != RRF_ACT_NONE || g.residual != nullptr
+               ? dispatch_mx<true>(g, a, b, sfa, sfb, sm_count, stream)
+               : dispatch_mx<false>(g, a, b, sfa, sfb, sm_count, stream);
 }
 
 cudaError_t launch_scaled_mm(const GemmArgs& g, const void* a, const void* b, int sm_count,
                              cudaStream_t stream) {
-    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, false, sm_count);
-    if (p.kernel == kGemmPair) return launch_pair(g, a, b, sm_count, stream);
-    if (p.kernel == kGemmSwap) {
-        if (p.a_rows == 8) return launch_swap_pairk<8, 8>(g, a, b, sm_count, stream);
-        if (p.a_rows == 16) return launch_swap_pairk<16, 4>(g, a, b, sm_count, stream);
-        return launch_swap_pairk<32, 4>(g, a, b, sm_count, stream);
-    }
-    if (p.tile_n == 128) return launch_bn<128, kBM, 1>(g, a, b, sm_count, stream);
-    if (p.a_rows == 64)
-        return p.k_tiles_per_stage == 4 ? launch_bn<64, 64, 4>(g, a, b, sm_count, stream)
-                                        : launch_bn<64, 64, 1>(g, a, b, sm_count, stream);
-    return p.k_tiles_per_stage == 2 ? launch_bn<64, kBM, 2>(g, a, b, sm_count, stream)
-                                    : launch_bn<64, kBM, 1>(g, a, b, sm_count, stream);
+    return g.act != RRF_ACT_NONE || g.residual != nullptr
+               ? dispatch<true>(g, a, b, sm_count, stream)
+               : dispatch<false>(g, a, b, sm_count, stream);
 }
 
 }  // namespace rrf

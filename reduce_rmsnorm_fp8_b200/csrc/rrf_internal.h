@@ -119,6 +119,8 @@ struct GemmArgs {
     int M, N, K;
     unsigned int* err;
     int starve;            // test hook: the epilogue's extra wait runs out
+    int act;               // RRF_ACT_*
+    const uint16_t* residual;  // bf16 [M, N] or null; may be out
 };
 
 // A [tokens, heads, head_dim] bf16 array (strides in elements; the head's

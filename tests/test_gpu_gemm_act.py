@@ -1,0 +1,236 @@
+"""GPU parity of the FP8 products with bias, activation and residual in their
+epilogue, against float64.
+
+Tolerance.  The sum's error E is the plain products' (see test_gpu_gemm.py):
+(K - 1) u sum|a b| + 3 u (|y| + |bias|), u = 2^-24.  An activation passes it on
+with a slope of at most 1.13 (gelu; silu 1.1, relu 1) and adds its own: the
+hardware exponential and quotient and erfc are within a few ulp of their
+arguments, and an argument z of the exponential (of erfc: z^2 / 2) rounded
+once moves the result by z u; results vanish below |z| = 104, so 2^-15
+relative covers it, and 2^-126 what underflows.  The residual's sum rounds
+once more, and the output to half a bf16 step (2^-8).
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+
+
+@pytest.fixture(scope="module")
+def rrf():
+    import reduce_rmsnorm_fp8_b200 as m
+    m.rrf_device_error(clear=True)
+    yield m
+    assert m.rrf_device_error() == 0
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def problem(rrf, seed, m, n, k, mx=False, bias=True, residual=True, spread=1.0):
+    """Operands whose products spread over +-`spread` and more."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    p = dict(mx=mx, m=m, n=n, k=k)
+    for name, rows, size in (("a", m, 1.0), ("b", n, spread / math.sqrt(k))):
+        x = randn(g, rows, k)
+        p[name] = x.clamp(-4, 4).mul(100).to(torch.float8_e4m3fn)
+        if mx:
+            code = torch.randint(118, 123, (rows, k // 32), generator=g, device="cuda").byte()
+            p["s" + name] = rrf.mx_blocked(code)
+            scale = torch.exp2(code.double() - 127).repeat_interleave(32, dim=1)
+            if name == "b":  # the product's size by the scales
+                code.sub_(max(0, round(math.log2(math.sqrt(k) / spread))))
+                p["sb"] = rrf.mx_blocked(code)
+                scale = torch.exp2(code.double() - 127).repeat_interleave(32, dim=1)
+        else:
+            s = (0.5 + torch.rand(rows, generator=g, device="cuda")) * size / 100
+            p["s" + name] = s
+            scale = s.double()[:, None]
+        p[name + "d"] = p[name].double() * scale
+    p["bias"] = randn(g, n).bfloat16() if bias else None
+    p["residual"] = randn(g, m, n).bfloat16() if residual else None
+    return p
+
+
+def activate(y, act):
+    """float64, without cancellation below 0."""
+    if act == "relu":
+        return y.clamp(min=0)
+    if act == "silu":
+        return y / (1 + torch.exp(-y))
+    if act == "gelu":
+        return 0.5 * y * torch.special.erfc(-y * math.sqrt(0.5))
+    if act == "gelu_tanh":
+        return y / (1 + torch.exp(-2 * math.sqrt(2 / math.pi) * (y + 0.044715 * y ** 3)))
+    return y
+
+
+def call(rrf, p, act, rows=None, **kw):
+    f = rrf.rrf_scaled_mm_mxfp8_act if p["mx"] else rrf.rrf_scaled_mm_fp8_act
+    return f(p["a"], p["sa"], p["b"], p["sb"], bias=p["bias"], activation=act,
+             residual=p["residual"], **kw)
+
+
+def check(p, got, act, residual, label=""):
+    rows = slice(None) if p["m"] <= 512 else torch.tensor(
+        sorted({0, 1, 127, 128, 255, 256, p["m"] // 2, p["m"] - 2, p["m"] - 1}), device="cuda")
+    ad = p["ad"][rows]
+    y, mag = ad @ p["bd"].T, ad.abs() @ p["bd"].abs().T
+    bias = 0.0 if p["bias"] is None else p["bias"].double()
+    err = (p["k"] - 1) * U * mag + 3 * U * (y.abs() + abs(bias))
+    z = activate(y + bias, act)
+    err = 1.13 * err + z.abs() * 2.0 ** -15 + 2.0 ** -126
+    if residual is not None:
+        z = z + residual[rows].double()
+        err = err + U * (z.abs() + err)
+    tol = err + 2.0 ** -8 * (z.abs() + err) + 2.0 ** -134
+    worst = float(((got[rows].double() - z).abs() / tol).max())
+    assert worst <= 1.0, f"{label} {act}: {worst:.3f} of the bound"
+
+
+# every kernel of the planner, per row / column scales and MX
+FP8 = [(1, 256, 128, "swap"), (9, 528, 640, "swap"), (24, 336, 1536, "swap"), (3, 320, 1152, "swap"),
+       (32, 7168, 512, "swap"), (5, 256, 144, "tile"), (64, 1024, 1024, "tile"),
+       (37, 256, 256, "tile"), (130, 400, 144, "tile"), (200, 272, 384, "tile"),
+       (1000, 2576, 272, "tile"), (2000, 2576, 1040, "pair"), (4096, 4112, 16, "pair")]
+MX = [(1, 256, 128, "swap"), (16, 208, 1408, "swap"), (29, 128, 1664, "swap"),
+      (60, 1040, 384, "tile"), (200, 272, 384, "tile"), (1000, 2576, 256, "tile"),
+      (2000, 2576, 640, "pair")]
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k,kernel,mx", [(*s, False) for s in FP8] + [(*s, True) for s in MX])
+def test_matches_float64(rrf, m, n, k, kernel, mx, act):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert rrf.rrf_plan_scaled_mm(m, n, k, sms, mx=mx)["kernel"] == kernel
+    for bias, residual in ((True, True), (False, True), (True, False), (False, False)):
+        p = problem(rrf, m + n + k, m, n, k, mx, bias, residual, spread=2.0)
+        check(p, call(rrf, p, act), act, p["residual"], f"bias {bias} residual {residual}")
+
+
+@pytest.mark.parametrize("m,n,k,mx", [(8, 16384, 1024, False), (32, 16384, 512, True),
+                                      (64, 16384, 512, False), (100, 16384, 256, True),
+                                      (4096, 4096, 512, False), (4096, 4096, 512, True)])
+def test_several_tiles_of_a_block(rrf, m, n, k, mx):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    plan = rrf.rrf_plan_scaled_mm(m, n, k, sms, mx=mx)
+    assert plan["tiles"] > plan["ctas"] // (2 if plan["kernel"] == "pair" else 1), plan
+    p = problem(rrf, m, m, n, k, mx)
+    check(p, call(rrf, p, "silu"), "silu", p["residual"])
+
+
+@pytest.mark.parametrize("m,mx", [(1, False), (20, True), (60, False), (300, False), (3000, True),
+                                  (3000, False)])
+def test_residual_in_place(rrf, m, mx):
+    p = problem(rrf, 7, m, 2064, 256, mx)
+    keep = p["residual"].clone()
+    out = call(rrf, p, "gelu", out=p["residual"])
+    assert out.data_ptr() == p["residual"].data_ptr()
+    check(p, out, "gelu", keep)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_without_epilogue_it_is_the_plain_product(rrf, mx):
+    for m in (1, 40, 150, 2048):
+        p = problem(rrf, m, m, 2048, 256, mx, residual=False)
+        plain = rrf.rrf_scaled_mm_mxfp8 if mx else rrf.rrf_scaled_mm_fp8
+        want = plain(p["a"], p["sa"], p["b"], p["sb"], p["bias"])
+        assert torch.equal(call(rrf, p, "none"), want)
+        # and a zero residual adds nothing but the sign of a zero
+        p["residual"] = torch.zeros_like(want)
+        assert torch.equal(call(rrf, p, "none"), want)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m", [4, 200])
+def test_far_values_of_the_activations(rrf, act, m):
+    """Sums from -1e30 to 1e30, each product one value: exact, so the error is
+    the activation's alone.  One side ends at 0 or keeps the value."""
+    n = k = 128
+    far = torch.tensor([0.0, 1e-30, 1e-4, 0.5, 3.0, 6.0, 9.0, 12.0, 30.0, 60.0, 88.0, 103.0,
+                        1e3, 1e10, 1e15, 1e30])
+    value = torch.cat((far, -far)).repeat(n // 32).cuda()
+    p = dict(mx=False, m=m, n=n, k=k, bias=None, residual=None,
+             a=torch.zeros((m, k), device="cuda"), b=torch.eye(n, device="cuda"),
+             sa=torch.ones(m, device="cuda"), sb=value)
+    p["a"][:, :] = 1.0
+    p["a"], p["b"] = (p[x].to(torch.float8_e4m3fn) for x in "ab")
+    got = call(rrf, p, act).double()
+    z = activate(value.double(), act)[None]
+    tol = z.abs() * (2.0 ** -15 + 2.0 ** -8) + 2.0 ** -126
+    assert not bool(got.isnan().any())
+    assert bool(((got - z).abs() <= tol).all())
+
+
+def test_infinities_and_nan_stay_in_their_place(rrf):
+    for m in (4, 40, 300, 2048):
+        p = problem(rrf, m, m, 2048, 256)
+        want = call(rrf, p, "silu")
+        p["residual"][1, 5] = float("nan")
+        p["residual"][2, 6] = float("inf")
+        got = call(rrf, p, "silu")
+        assert bool(got[1, 5].isnan()) and float(got[2, 6]) == float("inf")
+        got[1, 5], got[2, 6] = want[1, 5], want[2, 6]
+        assert torch.equal(got, want)
+
+
+def test_captured_and_on_another_stream(rrf):
+    p = problem(rrf, 3, 33, 1040, 384)
+    out = torch.empty((33, 1040), dtype=torch.bfloat16, device="cuda")
+    call(rrf, p, "gelu_tanh", out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(rrf, p, "gelu_tanh", out=out)
+    p["residual"].neg_()
+    out.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph.replay()
+    side.synchronize()
+    check(p, out, "gelu_tanh", p["residual"])
+
+
+def test_a_block_of_projections(rrf):
+    """The fused call's codes through an up projection with its activation,
+    and back down into the residual it wrote, in place."""
+    import parity
+    import workloads
+    c = parity.to_device(workloads.make_case("decode", 32, cols=1024))
+    q, s, h = rrf.rrf_sum_rmsnorm_fp8(c.inputs, c.gamma, c.eps, c.weight_offset, c.scale_ub,
+                                      residual_in=c.residual.clone())
+    up = problem(rrf, 1, 32, 2048, 1024, residual=False)
+    up.update(a=q, sa=s.reshape(-1), ad=q.double() * s.double())
+    mid = call(rrf, up, "silu")
+    check(up, mid, "silu", None, "up")
+    # the activations quantised by the same call (gamma 1)
+    one = torch.ones(2048, dtype=torch.bfloat16, device="cuda")
+    q2, s2, _ = rrf.rrf_sum_rmsnorm_fp8([mid], one, 1e-6, 0.0, float("inf"))
+    down = problem(rrf, 2, 32, 1024, 2048)
+    keep = h.clone()
+    down.update(a=q2, sa=s2.reshape(-1), ad=q2.double() * s2.double(), residual=h)
+    out = call(rrf, down, "none", out=h)
+    check(down, out, "none", keep, "down")
+
+
+def test_refusals_of_tensors(rrf):
+    p = problem(rrf, 1, 8, 64, 128)
+    args = (p["a"], p["sa"], p["b"], p["sb"])
+    f = rrf.rrf_scaled_mm_fp8_act
+    for bad in (dict(activation="tanh"), dict(residual=p["residual"][:4]),
+                dict(residual=p["residual"].float()), dict(residual=p["residual"].T),
+                dict(out=torch.empty((8, 64), device="cuda")), dict(bias=p["bias"][:10]),
+                dict(residual=p["residual"].cpu())):
+        with pytest.raises(ValueError):
+            f(*args, **bad)
+    with pytest.raises(rrf.RrfError) as e:  # a residual that only partly is out
+        buf = torch.empty(9 * 64, dtype=torch.bfloat16, device="cuda")
+        f(*args, residual=buf[:512].view(8, 64), out=buf[64:].view(8, 64))
+    assert e.value.status == rrf.Status.ERR_ALIAS
