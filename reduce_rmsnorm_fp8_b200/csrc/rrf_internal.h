@@ -156,9 +156,9 @@ struct HeadsArgs {
     float inv_dim;         // 1 / dim rounded to fp32
     float eps, weight_offset, scale_ub;
     unsigned int* err;
-    // set by the launcher: where the kinds of chunks begin, chunks and warps
-    // of a token
-    int key_chunk, value_chunk, chunks, warps_per_token;
+    // set by the launcher: where the kinds of chunks begin, the chunks of a
+    // token, and how many of them (or, writing alone, tokens) a warp takes
+    int key_chunk, value_chunk, chunks, per;
 };
 
 // Reading a cache back (rrf_cache.cu).
