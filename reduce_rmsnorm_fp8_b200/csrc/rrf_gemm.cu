@@ -1,5 +1,6 @@
 // rrf_gemm.cu -- the FP8 GEMM that consumes the per-row scales:
-//   out[m][n] = RN_bf16((sum_k a[m][k] * b[n][k]) * a_scale[m] * b_scale[n] + bias[n])
+//   out[m][n] = RN_bf16(act((sum_k a[m][k] * b[n][k]) * a_scale[m] * b_scale[n] + bias[n])
+//                       + residual[m][n])
 // on the 5th-generation tensor cores (Ascend CANN docs,
 // aclnnAlltoAllQuantMatmul: per-token dynamic quantisation of the
 // activations, then (x1_q @ x2) * x1Scale * x2Scale + bias).
@@ -14,7 +15,8 @@
 //            k-tiles of them per instruction); per-token and MX forms.
 // A persistent CTA per SM walks 128 x BN tiles of out (BN 128 or 64).
 // Warp roles (the same in every kernel; the swapped kernel's MX form adds a
-// seventh warp that rearranges the scale codes of each stage):
+// seventh warp that rearranges the scale codes of each stage, and tiles of 128
+// columns and more have eight epilogue warps):
 //   warp 0   one thread issues the TMA loads of the A (128 x 128 bytes) and
 //            B (BN x 128 bytes) k-tiles into a ring of shared-memory stages
 //            (128-byte swizzle, the layout the MMA descriptors name);
@@ -24,8 +26,9 @@
 //            tcgen05.commit per k-tile hands the stage back to the producer,
 //            one per tile hands the accumulator to the epilogue;
 //   warps 2-5 the epilogue: tcgen05.ld of its 32 accumulator lanes (rows),
-//            the two scales and bias, one rounding to bf16, 64-byte stores,
-//            while the MMAs of the next tile fill the other accumulator.
+//            the two scales, bias, activation and residual, one rounding to
+//            bf16, boxes taken out by TMA stores, while the MMAs of the next
+//            tile fill the other accumulator.
 // Every mbarrier wait is bounded in time; a wait that runs out sets
 // RRF_DEVICE_ERROR_GEMM_TIMEOUT, and the CTA still waits (bounded) for its
 // own loads and MMAs and frees its tensor memory before it returns.
@@ -182,126 +185,279 @@ __host__ __device__ constexpr uint32_t f8_idesc(int bn) {
 
 // ------------------------------------------------------------------ kernel --
 
-// The full epilogue (EPI kernels): out = RN_bf16(act(y) + residual), y the
-// scaled sum with its bias, all in fp32.  The activations, with the hardware's
-// exponential and quotient (a few ulp; the result is rounded to bf16, 2^16
-// times coarser):
+// ---------------------------------------------------------------- epilogue --
+//   out = RN_bf16(act(y) + residual),  y = (sum * a_scale) * b_scale + bias
+// in fp32 (the MX form without the scales, which act inside the MMA), one
+// rounding.  The activations:
 //   silu       y / (1 + e^-y)
-//   gelu       y erfc(-y / sqrt 2) / 2 (not 1 + erf, which cancels below 0)
 //   gelu_tanh  y (1 + tanh u) / 2 = y / (1 + e^-2u), u = sqrt(2 / pi)
 //              (y + 0.044715 y^3)
+//   gelu       y Phi(y) = max(y, 0) - |y| Q(|y|), Q(a) = erfc(a / sqrt 2) / 2
+//              (not 1 + erf, which cancels below 0)
+// with the hardware's exponential and reciprocal, a few ulp each: the result
+// is rounded to bf16, 2^16 times coarser.  All are written on pairs of values,
+// whose products and sums sm_100a does two at a time.
 
-// y / (1 + 2^t).  Both sides of the quotient are 2^-8 times that: the
-// approximate quotient is 0 for a divisor above 2^126, and so only where the
-// result is below 2^-126.
-__device__ __forceinline__ float over_one_plus_exp2(float y, float t) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t - 8.0f));
-    return __fdividef(y * 0.00390625f, 0.00390625f + e);
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// (2^t) and (1 / t) of both halves; results below 2^-126 are 0.
+__device__ __forceinline__ float2 exp2_pair(float2 t) {
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 reciprocal_pair(float2 t) {
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
+    return r;
+}
+
+// y / (1 + 2^(t + 8)).  Both sides of the quotient are 2^-8 times that: the
+// reciprocal is 0 for a divisor above 2^126, and so only where the result is
+// below 2^-126.
+__device__ __forceinline__ float2 over_one_plus_exp2(float2 y, float2 t) {
+    const float2 d = reciprocal_pair(__fadd2_rn(exp2_pair(t), both(0.00390625f)));
+    return __fmul2_rn(__fmul2_rn(y, both(0.00390625f)), d);
 }
 
 template <int ACT>
-__device__ __forceinline__ float activate(float y) {
+__device__ __forceinline__ float2 activate(float2 y) {
     constexpr float kLog2e = 1.44269504f;
-    if constexpr (ACT == RRF_ACT_RELU) return y < 0.0f ? 0.0f : y;  // (a NaN stays one)
-    if constexpr (ACT == RRF_ACT_SILU) return over_one_plus_exp2(y, -kLog2e * y);
-    if constexpr (ACT == RRF_ACT_GELU) return 0.5f * y * erfcf(-0.70710678f * y);
-    if constexpr (ACT == RRF_ACT_GELU_TANH)
-        return over_one_plus_exp2(y, -1.5957691f * kLog2e * (y + 0.044715f * y * y * y));
+    if constexpr (ACT == RRF_ACT_RELU)  // (a NaN stays one)
+        return make_float2(y.x < 0.0f ? 0.0f : y.x, y.y < 0.0f ? 0.0f : y.y);
+    if constexpr (ACT == RRF_ACT_SILU)
+        return over_one_plus_exp2(y, __ffma2_rn(y, both(-kLog2e), both(-8.0f)));
+    if constexpr (ACT == RRF_ACT_GELU_TANH) {
+        constexpr float k = -1.5957691216f * kLog2e;  // -2 sqrt(2 / pi) log2 e
+        const float2 c = __ffma2_rn(__fmul2_rn(y, y), both(0.044715f * k), both(k));
+        return over_one_plus_exp2(y, __ffma2_rn(y, c, both(-8.0f)));
+    }
+    if constexpr (ACT == RRF_ACT_GELU) {
+        // Q(a) = e^(-a^2 / 2) R(t), t = 1 / (1 + 0.3 a), R a polynomial fitted
+        // to erfcx(a / sqrt 2) / 2 over 0 <= a <= 14 (least maximum relative
+        // error, 1.9e-6; the exponential is 0 before a = 14)
+        const float2 a = make_float2(fminf(fabsf(y.x), 1e18f), fminf(fabsf(y.y), 1e18f));
+        const float2 t = reciprocal_pair(__ffma2_rn(a, both(0.3f), both(1.0f)));
+        float2 r = __ffma2_rn(t, both(-8.45932370e-02f), both(2.40572812e-01f));
+        r = __ffma2_rn(r, t, both(-4.86444432e-02f));
+        r = __ffma2_rn(r, t, both(1.64764484e-01f));
+        r = __ffma2_rn(r, t, both(1.06704533e-01f));
+        r = __ffma2_rn(r, t, both(1.21274699e-01f));
+        r = __ffma2_rn(r, t, both(-7.97889784e-05f));
+        const float2 e = exp2_pair(__fmul2_rn(__fmul2_rn(a, both(-0.5f * kLog2e)), a));
+        const float2 q = __fmul2_rn(__fmul2_rn(a, both(-1.0f)), __fmul2_rn(e, r));
+        // max(y, 0), keeping a NaN
+        const float2 p = make_float2(__fmaf_rn(0.5f, y.x, 0.5f * fabsf(y.x)),
+                                     __fmaf_rn(0.5f, y.y, 0.5f * fabsf(y.y)));
+        return __fadd2_rn(p, q);
+    }
     return y;
 }
 
-template <int N>
-__device__ __forceinline__ void activate_all(int act, float y[N]) {
-    if (act == RRF_ACT_RELU) {
+template <int ACT, int PAIRS>
+__device__ __forceinline__ void activate_pairs(float2 y[PAIRS]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = activate<RRF_ACT_RELU>(y[i]);
-    } else if (act == RRF_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = activate<RRF_ACT_SILU>(y[i]);
-    } else if (act == RRF_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = activate<RRF_ACT_GELU>(y[i]);
-    } else if (act == RRF_ACT_GELU_TANH) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = activate<RRF_ACT_GELU_TANH>(y[i]);
-    }
+    for (int i = 0; i < PAIRS; ++i) y[i] = activate<ACT>(y[i]);
 }
 
-// 16 bytes of a residual, which may be the output itself: a coherent load that
-// stays where it is written (behind the wait for the previous kernel).
-__device__ __forceinline__ uint4 ld_residual(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
+// (one branch for all the values)
+template <int PAIRS>
+__device__ __forceinline__ void activate_all(int act, float2 y[PAIRS]) {
+    if (act == RRF_ACT_NONE) return;
+    if (act == RRF_ACT_RELU) activate_pairs<RRF_ACT_RELU, PAIRS>(y);
+    else if (act == RRF_ACT_SILU) activate_pairs<RRF_ACT_SILU, PAIRS>(y);
+    else if (act == RRF_ACT_GELU) activate_pairs<RRF_ACT_GELU, PAIRS>(y);
+    else activate_pairs<RRF_ACT_GELU_TANH, PAIRS>(y);
+}
+
+// The epilogue of a warp's 32 rows (one accumulator lane each), 64 columns (a
+// chunk) at a time.  A lane holds a row, but memory is read and written in
+// boxes of 32 rows x 128 bytes: a TMA load brings the residual's box into
+// shared memory a chunk ahead, each lane adds its row to it in place, and a
+// TMA store takes the box out (rows and columns past the matrix are not
+// written).  Boxes are 128-byte swizzled: 16-byte piece p of row r sits at
+// p ^ (r % 8), so that a column of rows does not meet in a bank.  The scales
+// and the bias of the chunk's columns are loaded a chunk ahead too.
+// B200, 4096 x 4096 x 1024 with silu and residual: 88.9 us with each lane
+// reading and writing its own row 64 bytes at a time and its column scales one
+// by one; 35.1 us through shared memory with the warp's own coalesced loads
+// and stores; 32.5 us with TMA.  (The products alone take 15 us there: at so
+// short a K the epilogue's shared-memory traffic, 5 passes over 64 KB a tile,
+// meets the operands' in the same banks.)
+constexpr int kChunk = 64;               // columns of a chunk
+constexpr int kBoxBytes = 32 * kChunk * 2;
+
+// Of `warps` epilogue warps with `boxes` boxes each: the boxes (1024-byte
+// aligned), per warp a (scale, scale, bias, bias) for each pair of columns,
+// and per box a barrier.
+template <int WARPS, int BOXES>
+struct EpiLayout {
+    static constexpr int kColumns = WARPS * BOXES * kBoxBytes;
+    static constexpr int kBarriers = kColumns + WARPS * kChunk * 8;
+    static constexpr int kBytes = kBarriers + WARPS * BOXES * 8;
+};
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x,
+                                             int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 :: "l"(map), "r"(smem_u32(src)), "r"(x), "r"(y)
                  : "memory");
-    return v;
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// The epilogue of 32 accumulator columns [n, n + 32) of one output row: both
-// scales and the bias in fp32, one rounding to bf16, 64-byte stores (16 or
-// 32 columns valid: N % 16 == 0).
-template <bool EPI>
-__device__ __forceinline__ void store_row_chunk(const GemmArgs& g, const float v[32], float sa,
-                                                int row, int n) {
-    if (!RRF_IN_BOUNDS(row >= 0 && row < g.M && n >= 0 && n < g.N, g.err)) return;
-    const int valid = g.N - n < 32 ? g.N - n : 32;
-    uint32_t packed[16];
-    if constexpr (EPI) {
-        uint4 res[4];
-        const uint4* src = reinterpret_cast<const uint4*>(g.residual + (int64_t)row * g.N + n);
-        if (g.residual != nullptr) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (q * 8 < valid) res[q] = ld_residual(src + q);
+// Make this thread's shared-memory stores visible to the async proxy
+// (tcgen05.cp and TMA stores read them).
+__device__ __forceinline__ void fence_proxy_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// One epilogue warp: chunk() works on the chunks of its tiles in turn.
+template <int WARPS, int BOXES, bool SCALED>
+struct EpiWarp {
+    using L = EpiLayout<WARPS, BOXES>;
+    const GemmArgs& g;
+    const CUtensorMap* res_map;
+    const CUtensorMap* out_map;
+    uint8_t* boxes;
+    float4* columns;
+    uint64_t* bars;
+    int lane;
+    int count;           // chunks inside the matrix so far; chunk k has box k % BOXES
+    bool loading;        // the next chunk's residual box is on its way
+    float2 scale, bias;  // of the next chunk's columns 2 lane, 2 lane + 1
+
+    __device__ __forceinline__ EpiWarp(const GemmArgs& args, const CUtensorMap* rm,
+                                       const CUtensorMap* om, uint8_t* area, int warp, int l)
+        : g(args), res_map(rm), out_map(om), boxes(area + warp * BOXES * kBoxBytes),
+          columns(reinterpret_cast<float4*>(area + L::kColumns + warp * kChunk * 8)),
+          bars(reinterpret_cast<uint64_t*>(area + L::kBarriers) + warp * BOXES), lane(l),
+          count(0), loading(false), scale(both(1.0f)), bias(both(-0.0f)) {}
+
+    static __device__ __forceinline__ void init_barriers(uint8_t* area) {
+        for (int i = 0; i < WARPS * BOXES; ++i)
+            mbar_init(reinterpret_cast<uint64_t*>(area + L::kBarriers) + i, 1);
+    }
+
+    // Begin the loads of the next chunk, rows row0 .., columns n ...
+    __device__ __forceinline__ void ahead(int row0, int n) {
+        load_columns(n);
+        load_box(row0, n);
+    }
+
+    // Lane 0: no store reads a box any more.
+    __device__ __forceinline__ void boxes_free() const {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+
+    // The chunk at rows row0 .., columns n .., its accumulator at `taddr` (this
+    // warp's lanes), sa the lane's row scale; the next one is at row_next,
+    // n_next (more == false: there is none).  after_read() runs when the
+    // accumulator's columns have been read.  False if a wait ran out.
+    template <class AfterRead>
+    __device__ __forceinline__ bool chunk(uint32_t taddr, float sa, int row0, int n, bool more,
+                                          int row_next, int n_next, AfterRead after_read) {
+        uint4* box = reinterpret_cast<uint4*>(boxes + (count % BOXES) * kBoxBytes);
+        if (loading) {
+            loading = false;
+            const bool ok = wait_phase(&bars[count % BOXES], (count / BOXES) & 1, g.err);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return false;
         }
-        float y[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            y[i] = v[i];
-            if (g.b_scale != nullptr && i < valid)
-                y[i] = __fmul_rn(__fmul_rn(v[i], sa), g.b_scale[n + i]);
-            if (g.bias != nullptr && i < valid)
-                y[i] = __fadd_rn(y[i], __uint_as_float((uint32_t)g.bias[n + i] << 16));
+        if (!inside(row0, n)) {  // uniform in the warp
+            after_read();
+            if (more) {
+                boxes_free();
+                ahead(row_next, n_next);
+            }
+            __syncwarp();
+            return true;
         }
-        activate_all<32>(g.act, y);
-        if (g.residual != nullptr) {
+        ++count;
+        columns[lane] = make_float4(scale.x, scale.y, bias.x, bias.y);
+        __syncwarp();
+        if (more) load_columns(n_next);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (q * 8 < valid) {
-                    float r[8];
-                    bf16x8_to_f32(res[q], r);
+        for (int h = 0; h < 2; ++h) {
+            float v[32];
+            tmem_load_32(taddr + 32 * h, v);
+            if (h == 1) after_read();
+            float2 y[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[8 * q + i] = __fadd_rn(y[8 * q + i], r[i]);
+            for (int i = 0; i < 16; ++i) {
+                const float4 s = columns[16 * h + i];
+                y[i] = make_float2(v[2 * i], v[2 * i + 1]);
+                if constexpr (SCALED)
+                    y[i] = __fmul2_rn(__fmul2_rn(y[i], both(sa)), make_float2(s.x, s.y));
+                y[i] = __fadd2_rn(y[i], make_float2(s.z, s.w));
+            }
+            activate_all<16>(g.act, y);
+            uint4* row = box + lane * 8;
+            if (g.residual != nullptr) {
+                uint4 res[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) res[q] = row[(4 * h + q) ^ (lane & 7)];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float2 r[4];
+                    bf16x8_to_f32x2(res[q], r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[4 * q + i] = __fadd2_rn(y[4 * q + i], r[i]);
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) packed[i / 2] = f32x2_to_bf16x2(y[i], y[i + 1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            // (the MX GEMM has no column scales: its scales act inside the MMA)
-            const float s0 = i < valid ? (g.b_scale != nullptr ? g.b_scale[n + i] : 1.0f) : 0.0f;
-            const float s1 =
-                i + 1 < valid ? (g.b_scale != nullptr ? g.b_scale[n + i + 1] : 1.0f) : 0.0f;
-            float y0 = __fmul_rn(__fmul_rn(v[i], sa), s0);
-            float y1 = __fmul_rn(__fmul_rn(v[i + 1], sa), s1);
-            if (g.bias != nullptr && i < valid) {
-                y0 = __fadd_rn(y0, __uint_as_float((uint32_t)g.bias[n + i] << 16));
-                y1 = __fadd_rn(y1, __uint_as_float((uint32_t)g.bias[n + i + 1] << 16));
+            for (int q = 0; q < 4; ++q)
+                row[(4 * h + q) ^ (lane & 7)] = f32x2_to_bf16x8(y + 4 * q);
+            if (h == 0 && BOXES > 1) {
+                // the other box's store began a chunk ago
+                boxes_free();
+                if (more) load_box(row_next, n_next);
             }
-            packed[i / 2] = f32x2_to_bf16x2(y0, y1);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tma_store_2d(out_map, box, n, row0);
+        if (BOXES == 1) {
+            boxes_free();
+            if (more) load_box(row_next, n_next);
+        }
+        __syncwarp();
+        return true;
+    }
+
+    // Before the block's end: its stores have read their boxes, and (after a
+    // wait that ran out) the residual on its way has landed.
+    __device__ __forceinline__ void finish() {
+        if (loading) wait_phase(&bars[count % BOXES], (count / BOXES) & 1, g.err);
+        boxes_free();
+    }
+
+  private:
+    __device__ __forceinline__ bool inside(int row0, int n) const {
+        return row0 < g.M && n < g.N && RRF_IN_BOUNDS(row0 >= 0 && n >= 0, g.err);
+    }
+
+    __device__ __forceinline__ void load_box(int row0, int n) {
+        if (g.residual == nullptr || !inside(row0, n)) return;
+        loading = true;
+        if (lane == 0) {
+            uint64_t* bar = &bars[count % BOXES];
+            mbar_arrive_expect_tx(bar, kBoxBytes);
+            tma_load_2d(boxes + (count % BOXES) * kBoxBytes, res_map, bar, n, row0);
         }
     }
-    uint4* dst = reinterpret_cast<uint4*>(g.out + (int64_t)row * g.N + n);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (q * 8 < valid)
-            dst[q] = make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2],
-                                packed[4 * q + 3]);
-}
+
+    // (a bias that is not there is -0, which leaves every value as it is)
+    __device__ __forceinline__ void load_columns(int n) {
+        const int col = n + 2 * lane;
+        if (col >= g.N) return;  // (N is even)
+        if constexpr (SCALED) scale = make_float2(g.b_scale[col], g.b_scale[col + 1]);
+        if (g.bias != nullptr)
+            bias = make_float2(__uint_as_float((uint32_t)g.bias[col] << 16),
+                               __uint_as_float((uint32_t)g.bias[col + 1] << 16));
+    }
+};
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
@@ -327,16 +483,21 @@ struct Tile {
     static constexpr int kBBytes = BN * kBK;           // one k-tile of B
     static constexpr int kBOffset = Z * kABytes;       // B tiles follow the Z A tiles
     static constexpr int kStageBytes = Z * (kABytes + kBBytes);
-    // as many stages as fit in 200 KB (220 KB with several k-tiles per
-    // stage), at most 12: 4 at BN 256, 6 at 128, 8 at 64, 12 with 64-row A
-    // stages, 3 with four k-tiles of 64 rows
-    static constexpr int kBudget = (Z > 1 ? 220 : 200) * 1024;
+    // an epilogue warp for each 32 rows and each 64 columns
+    static constexpr int kEpiWarps = 4 * (BN / kChunk);
+    static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
+    // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 8
+    // at 64, 12 with 64-row A stages, 3 with four k-tiles of 64 rows
+    using Epi = EpiWarp<kEpiWarps, 1, true>;
+    static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
     static constexpr int kStages = kBudget / kStageBytes > 12 ? 12 : kBudget / kStageBytes;
     static constexpr int kTmemCols = 2 * BN;  // two accumulators
     // full / empty per stage, full / empty per accumulator, one for the drain
     static constexpr int kBarriers = 2 * kStages + 4 + 1;
+    static constexpr int kEpiOffset = kStages * kStageBytes;
+    static constexpr int kBarrierOffset = kEpiOffset + Epi::L::kBytes;
     // 1 KB of slack aligns the stages to the 1024-byte swizzle atom
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarriers * 8 + 16;
+    static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
     static_assert(kSmemBytes <= 227 * 1024, "stages exceed the shared memory of a CTA");
 };
 
@@ -371,16 +532,18 @@ __device__ __forceinline__ void load_group(uint8_t* dst, const CUtensorMap* ma,
 // the 128 x BN tiles, so the CTAs working at one time share A rows and B
 // columns in L2).  The accumulator is double-buffered in tensor memory: the
 // MMAs of a CTA's next tile run while the epilogue warps drain this one.
-template <int BN, int AROWS, int Z, bool EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int BN, int AROWS, int Z>
+__global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
     scaled_mm_kernel(const __grid_constant__ CUtensorMap tma_a,
-                     const __grid_constant__ CUtensorMap tma_b, const GemmArgs g) {
+                     const __grid_constant__ CUtensorMap tma_b,
+                     const __grid_constant__ CUtensorMap tma_res,
+                     const __grid_constant__ CUtensorMap tma_out, const GemmArgs g) {
     using T = Tile<BN, AROWS, Z>;
     constexpr int S = T::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * T::kStageBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::kBarrierOffset);
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;       // [2]: the tile's MMAs are done
     uint64_t* acc_empty = acc_full + 2;   // [2]: the epilogue has read the tile
@@ -400,9 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);  // one arrival per epilogue warp
+            mbar_init(&acc_empty[b], T::kEpiWarps);  // one arrival per epilogue warp
         }
         mbar_init(drained, 1);
+        T::Epi::init_barriers(smem + T::kEpiOffset);
         fence_mbar_init_cluster();
     }
     if (warp == 1) {
@@ -486,30 +650,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- epilogue: warp w reads accumulator lanes 32 * (w % 4) ...
-        const int quarter = warp & 3;
+        // ---- epilogue: warp w reads accumulator lanes 32 * (w % 4) ... and
+        // 64 columns
+        const int quarter = warp & 3, c = ((warp - 2) >> 2) * kChunk;
+        typename T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, warp - 2, lane);
+        int row0 = (blockIdx.x / tiles_n) * kBM + quarter * 32, n = (blockIdx.x % tiles_n) * BN + c;
+        epi.ahead(row0, n);
         int j = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
             const int buf = j & 1;
-            const int m0 = (t / tiles_n) * kBM, n0 = (t % tiles_n) * BN;
+            const int next = t + gridDim.x;
+            const int row_next = (next / tiles_n) * kBM + quarter * 32;
+            const int n_next = (next % tiles_n) * BN + c;
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
             if (!__all_sync(0xFFFFFFFFu, have)) break;
             tc_fence_after_sync();
-            const int row = m0 + quarter * 32 + lane;
-            const float sa = row < g.M ? g.a_scale[row] : 0.0f;
-            const uint32_t base = tmem + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
-            for (int c = 0; c < BN; c += 32) {
-                float v[32];
-                tmem_load_32(base + (uint32_t)c, v);
-                const int n = n0 + c;
-                if (row >= g.M || n >= g.N) continue;
-                store_row_chunk<EPI>(g, v, sa, row, n);
-            }
-            // this warp's reads of the accumulator are done: hand it back
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            const float sa = row0 + lane < g.M ? g.a_scale[row0 + lane] : 0.0f;
+            if (!epi.chunk(tmem + (uint32_t)(buf * BN + c) + ((uint32_t)(quarter * 32) << 16), sa,
+                           row0, n, next < tiles, row_next, n_next, [&]() {
+                               // this warp's reads of the accumulator are done:
+                               // hand it back
+                               tc_fence_before_sync();
+                               __syncwarp();
+                               if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                           }))
+                break;
+            row0 = row_next;
+            n = n_next;
         }
+        epi.finish();
     }
 
     // ---- teardown: tensor memory is freed after the CTA's last MMA and load
@@ -640,15 +809,12 @@ struct SwapPairTile {
     static_assert(kXBytes % 1024 == 0, "each k-tile must start on a swizzle atom");
 };
 
-// Make this thread's shared-memory stores visible to the async proxy
-// (tcgen05.cp reads them).
-__device__ __forceinline__ void fence_proxy_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// A bf16 value of memory the kernel may also write (a residual in place).
-__device__ __forceinline__ float bf16_at(const uint16_t* p) {
-    return __uint_as_float((uint32_t)*reinterpret_cast<const volatile uint16_t*>(p) << 16);
+// One bf16 of a residual, which may be the output itself: a coherent load that
+// stays where it is written (behind the wait for the previous kernel).
+__device__ __forceinline__ uint16_t ld_residual(const uint16_t* p) {
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    return v;
 }
 
 // NA consecutive fp32 accumulator columns of this thread's lane (NA = 8, 16
@@ -683,7 +849,7 @@ __device__ __forceinline__ void tmem_load_cols(uint32_t taddr, float v[NA]) {
 
 // sfx, sfw: the MX form's scale codes of the call's rows and of the weight
 // (the blocked order); null in the per-token form.
-template <int NA, int Z, bool MX, bool EPI>
+template <int NA, int Z, bool MX>
 __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
     scaled_mm_swap_pairk_kernel(const __grid_constant__ CUtensorMap tma_x,
                                 const __grid_constant__ CUtensorMap tma_w, const GemmArgs g,
@@ -916,6 +1082,18 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
             const int buf = j & 1;
             const int n = t * T::kWRows + w;
+            // what the even warps add, ahead of the accumulator
+            uint16_t res[NA];
+            float sb = 1.0f, bias = 0.0f;
+            if (!odd && n < g.N) {
+                if constexpr (!MX) sb = g.b_scale[n];
+                if (g.bias != nullptr) bias = __uint_as_float((uint32_t)g.bias[n] << 16);
+                if (g.residual != nullptr) {
+#pragma unroll
+                    for (int m = 0; m < NA; ++m)
+                        if (m < g.M) res[m] = ld_residual(g.residual + (int64_t)m * g.N + n);
+                }
+            }
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
             if (!__all_sync(0xFFFFFFFFu, have)) break;
             tc_fence_after_sync();
@@ -934,43 +1112,33 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
                 mbar_arrive(comb_full);  // each thread releases its own stores
             } else {
                 if (!wait_phase(comb_full, j & 1, g.err)) ok = false;
-                float o[NA];
+                float2 y[NA / 2];
 #pragma unroll
-                for (int m = 0; m < NA; ++m) o[m] = comb[m * T::kWRows + w];
+                for (int m = 0; m < NA / 2; ++m) {
+                    y[m].x = __fadd_rn(v[2 * m], comb[2 * m * T::kWRows + w]);
+                    y[m].y = __fadd_rn(v[2 * m + 1], comb[(2 * m + 1) * T::kWRows + w]);
+                }
                 mbar_arrive(comb_empty);
                 if (ok && n < g.N && RRF_IN_BOUNDS(n >= 0, g.err)) {
-                    const float sb = MX ? 1.0f : g.b_scale[n];
-                    const float bias =
-                        g.bias != nullptr ? __uint_as_float((uint32_t)g.bias[n] << 16) : 0.0f;
-                    if constexpr (EPI) {
-                        // NA values at once, so that the activation's branch
-                        // is taken once
 #pragma unroll
-                        for (int m = 0; m < NA; ++m) {
-                            o[m] = __fadd_rn(v[m], o[m]);
-                            if constexpr (!MX)
-                                if (m < g.M)
-                                    o[m] = __fmul_rn(__fmul_rn(o[m], __ldg(g.a_scale + m)), sb);
-                            if (g.bias != nullptr) o[m] = __fadd_rn(o[m], bias);
+                    for (int m = 0; m < NA / 2; ++m) {
+                        if constexpr (!MX) {
+                            const float2 sa =
+                                make_float2(2 * m < g.M ? __ldg(g.a_scale + 2 * m) : 0.0f,
+                                            2 * m + 1 < g.M ? __ldg(g.a_scale + 2 * m + 1) : 0.0f);
+                            y[m] = __fmul2_rn(__fmul2_rn(y[m], sa), both(sb));
                         }
-                        activate_all<NA>(g.act, o);
+                        if (g.bias != nullptr) y[m] = __fadd2_rn(y[m], both(bias));
                     }
+                    activate_all<NA / 2>(g.act, y);
 #pragma unroll
                     for (int m = 0; m < NA; ++m) {
                         if (m < g.M) {
-                            float y;
-                            if constexpr (EPI) {
-                                y = o[m];
-                                if (g.residual != nullptr)
-                                    y = __fadd_rn(y, bf16_at(g.residual + (int64_t)m * g.N + n));
-                            } else {
-                                y = __fadd_rn(v[m], o[m]);
-                                if constexpr (!MX)
-                                    y = __fmul_rn(__fmul_rn(y, __ldg(g.a_scale + m)), sb);
-                                if (g.bias != nullptr) y = __fadd_rn(y, bias);
-                            }
+                            float z = m % 2 ? y[m / 2].y : y[m / 2].x;
+                            if (g.residual != nullptr)
+                                z = __fadd_rn(z, __uint_as_float((uint32_t)res[m] << 16));
                             g.out[(int64_t)m * g.N + n] =
-                                (uint16_t)(f32x2_to_bf16x2(y, 0.0f) & 0xFFFFu);
+                                (uint16_t)(f32x2_to_bf16x2(z, 0.0f) & 0xFFFFu);
                         }
                     }
                 }
@@ -1006,9 +1174,12 @@ __device__ __forceinline__ uint32_t peer_smem(const void* local, uint32_t rank) 
     return r;
 }
 
-// One arrival on an mbarrier given by its shared::cluster address.
+// One arrival on an mbarrier given by its shared::cluster address.  Relaxed:
+// it hands back tensor memory, whose reads have completed (tcgen05.wait::ld
+// and the fence before); a release at cluster scope would also wait until
+// this warp's output stores are visible.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar)
                  : "memory");
 }
 
@@ -1076,26 +1247,37 @@ __device__ __forceinline__ void grouped_tile(int t, int tiles_m, int tiles_n, in
     tn = r / rows;
 }
 
+// Eight epilogue warps in each CTA of a pair: two for each 32 rows, on every
+// other 64 columns.
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kPairBoxes = 2;   // of each epilogue warp (1 and a fifth stage: 25% slower at K = 1024)
+constexpr int kPairStages = 4;
+
 struct PairTile {
     static constexpr int kHalfBytes = 128 * kBK;            // 16 KB: 128 rows of A or of B
     static constexpr int kStageBytes = 2 * kHalfBytes;      // this CTA's A half and B half
-    static constexpr int kStages = 6;                       // 192 KB (7 measured no faster)
+    static constexpr int kStages = kPairStages;             // 128 KB
     static constexpr int kTmemCols = 512;                   // two 256-column accumulators
     static constexpr int kBarriers = 2 * kStages + 4 + 1;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarriers * 8 + 16;
+    using Epi = EpiWarp<kPairEpiWarps, kPairBoxes, true>;
+    static constexpr int kEpiOffset = kStages * kStageBytes;
+    static constexpr int kBarrierOffset = kEpiOffset + Epi::L::kBytes;
+    static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
 };
 
-template <bool EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     scaled_mm_pair_kernel(const __grid_constant__ CUtensorMap tma_a,
-                          const __grid_constant__ CUtensorMap tma_b, const GemmArgs g) {
+                          const __grid_constant__ CUtensorMap tma_b,
+                          const __grid_constant__ CUtensorMap tma_res,
+                          const __grid_constant__ CUtensorMap tma_out, const GemmArgs g) {
     using T = PairTile;
     constexpr int S = T::kStages;
     constexpr int BN = 256;  // the pair tile is 256 x 256
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * T::kStageBytes);  // leader's are used
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::kBarrierOffset);  // leader's are used
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;       // [2]
     uint64_t* acc_empty = acc_full + 2;   // [2], the leader's: both CTAs' epilogue warps
@@ -1116,9 +1298,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);  // 4 epilogue warps in each CTA of the pair
+            mbar_init(&acc_empty[b], 2 * kPairEpiWarps);  // both CTAs'
         }
         mbar_init(drained, 1);
+        T::Epi::init_barriers(smem + T::kEpiOffset);
         fence_mbar_init_cluster();
     }
     if (warp == 1) {
@@ -1204,32 +1387,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ---- epilogue (each CTA): its 128 accumulator rows of the tile
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, warp - 2, lane);
         const uint32_t leader_acc_empty[2] = {peer_smem(&acc_empty[0], 0),
                                               peer_smem(&acc_empty[1], 0)};
+        int tm, tn;
+        grouped_tile(pair, tiles_m, tiles_n, tm, tn);
+        int row0 = tm * 256 + (int)rank * 128 + quarter * 32, n0 = tn * 256 + group * kChunk;
+        epi.ahead(row0, n0);
         int j = 0;
         for (int t = pair; t < tiles; t += npairs, ++j) {
             const int buf = j & 1;
-            int tm, tn;
-            grouped_tile(t, tiles_m, tiles_n, tm, tn);
-            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256;
+            const bool more = t + npairs < tiles;
+            if (more) grouped_tile(t + npairs, tiles_m, tiles_n, tm, tn);
+            const int row_next = tm * 256 + (int)rank * 128 + quarter * 32;
+            const int n_next = tn * 256 + group * kChunk;
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
             if (!__all_sync(0xFFFFFFFFu, have)) break;
             tc_fence_after_sync();
-            const int row = m0 + quarter * 32 + lane;
-            const float sa = row < g.M ? g.a_scale[row] : 0.0f;
-            const uint32_t base = tmem + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
-            for (int c = 0; c < BN; c += 32) {
-                float v[32];
-                tmem_load_32(base + (uint32_t)c, v);
-                const int n = n0 + c;
-                if (row >= g.M || n >= g.N) continue;
-                store_row_chunk<EPI>(g, v, sa, row, n);
-            }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_acc_empty[buf]);
+            const float sa = row0 + lane < g.M ? g.a_scale[row0 + lane] : 0.0f;
+            const uint32_t base = tmem + (uint32_t)(buf * BN + group * kChunk) +
+                                  ((uint32_t)(quarter * 32) << 16);
+            if (!epi.chunk(base, sa, row0, n0, true, row0, n0 + 128, [] {})) break;
+            if (!epi.chunk(base + 128, sa, row0, n0 + 128, more, row_next, n_next, [&]() {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(leader_acc_empty[buf]);
+                }))
+                break;
+            row0 = row_next;
+            n0 = n_next;
         }
+        epi.finish();
     }
 
     // ---- teardown: every MMA of the pair is done before tensor memory is
@@ -1272,29 +1461,36 @@ struct MxTile {
     static constexpr int kSfbOffset = kSfaOffset + Z * kSfBytes;
     static constexpr int kStageBytes = Z * (kABytes + kBBytes + 2 * kSfBytes);
     static constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-    // as many stages as fit in 200 KB (220 KB with several k-tiles per
-    // stage), at most 12: 6 at BN 128, 11 at 64, 3 with four 64-row k-tiles
-    static constexpr int kBudget = (Z > 1 ? 220 : 200) * 1024;
+    static constexpr int kEpiWarps = 4 * (BN / kChunk);
+    static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
+    // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 4
+    // at 64, 3 with four 64-row k-tiles
+    using Epi = EpiWarp<kEpiWarps, 1, false>;
+    static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
     static constexpr int kStages = kBudget / kStageStride > 12 ? 12 : kBudget / kStageStride;
     static constexpr int kAccCols = 2 * BN;          // two accumulators
     // accumulators, then 4 + 4 scale columns (a power of two of at least 32)
     static constexpr int kTmemCols = BN == 128 ? 512 : 256;
     static constexpr int kBarriers = 2 * kStages + 4 + 1;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageStride + kBarriers * 8 + 16;
+    static constexpr int kEpiOffset = kStages * kStageStride;
+    static constexpr int kBarrierOffset = kEpiOffset + Epi::L::kBytes;
+    static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
     static_assert(kSmemBytes <= 227 * 1024, "stages exceed the shared memory of a CTA");
 };
 
-template <int BN, int AROWS, int Z, bool EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int BN, int AROWS, int Z>
+__global__ void __launch_bounds__(MxTile<BN, AROWS, Z>::kThreadsPerCta, 1)
     scaled_mm_mx_kernel(const __grid_constant__ CUtensorMap tma_a,
-                        const __grid_constant__ CUtensorMap tma_b, const GemmArgs g,
+                        const __grid_constant__ CUtensorMap tma_b,
+                        const __grid_constant__ CUtensorMap tma_res,
+                        const __grid_constant__ CUtensorMap tma_out, const GemmArgs g,
                         const uint8_t* sfa, const uint8_t* sfb) {
     using T = MxTile<BN, AROWS, Z>;
     constexpr int S = T::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * T::kStageStride);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::kBarrierOffset);
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;
     uint64_t* acc_empty = acc_full + 2;
@@ -1314,9 +1510,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], T::kEpiWarps);
         }
         mbar_init(drained, 1);
+        T::Epi::init_barriers(smem + T::kEpiOffset);
         fence_mbar_init_cluster();
     }
     if (warp == 1) {
@@ -1414,28 +1611,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- epilogue: the scales are inside the accumulator; bias, bf16
-        const int quarter = warp & 3;
+        // ---- epilogue: the scales are inside the accumulator
+        const int quarter = warp & 3, c = ((warp - 2) >> 2) * kChunk;
+        typename T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, warp - 2, lane);
+        int row0 = (blockIdx.x / tiles_n) * kBM + quarter * 32, n = (blockIdx.x % tiles_n) * BN + c;
+        epi.ahead(row0, n);
         int j = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
             const int buf = j & 1;
-            const int m0 = (t / tiles_n) * kBM, n0 = (t % tiles_n) * BN;
+            const int next = t + gridDim.x;
+            const int row_next = (next / tiles_n) * kBM + quarter * 32;
+            const int n_next = (next % tiles_n) * BN + c;
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
             if (!__all_sync(0xFFFFFFFFu, have)) break;
             tc_fence_after_sync();
-            const int row = m0 + quarter * 32 + lane;
-            const uint32_t base = tmem + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
-            for (int c = 0; c < BN; c += 32) {
-                float v[32];
-                tmem_load_32(base + (uint32_t)c, v);
-                const int n = n0 + c;
-                if (row >= g.M || n >= g.N) continue;
-                store_row_chunk<EPI>(g, v, 1.0f, row, n);  // g.b_scale is null: no scaling
-            }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            const float sa = 1.0f;
+            if (!epi.chunk(tmem + (uint32_t)(buf * BN + c) + ((uint32_t)(quarter * 32) << 16), sa,
+                           row0, n, next < tiles, row_next, n_next, [&]() {
+                               // this warp's reads of the accumulator are done:
+                               // hand it back
+                               tc_fence_before_sync();
+                               __syncwarp();
+                               if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                           }))
+                break;
+            row0 = row_next;
+            n = n_next;
         }
+        epi.finish();
     }
 
     tc_fence_before_sync();
@@ -1508,31 +1711,35 @@ struct MxPairTile {
     static constexpr int kSfOffset = 2 * kHalfBytes;
     static constexpr int kStageBytes = 2 * kHalfBytes + kSfaBytes + kSfbBytes;  // 33.5 KB
     static constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;     // 34 KB
-    static constexpr int kStages = 6;
+    static constexpr int kStages = kPairStages;
     static constexpr int kTmemCols = 512;
     static constexpr uint32_t kBuf1 = 224;                       // buffer 1's first column
     static constexpr uint32_t kSfaCol = kBuf1 + BN;              // 480
     static constexpr uint32_t kSfbCol = kSfaCol + 4;             // 484 .. 491
     // full / empty per stage, full / empty per accumulator, overlap, drain
     static constexpr int kBarriers = 2 * kStages + 4 + 1 + 1;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageStride + kBarriers * 8 + 16;
+    using Epi = EpiWarp<kPairEpiWarps, kPairBoxes, false>;
+    static constexpr int kEpiOffset = kStages * kStageStride;
+    static constexpr int kBarrierOffset = kEpiOffset + Epi::L::kBytes;
+    static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
 };
 static_assert(MxPairTile::kSfbCol + 8 <= MxPairTile::kTmemCols, "scale columns past the allocation");
 static_assert(MxPairTile::kSmemBytes <= 227 * 1024, "stages exceed the shared memory of a CTA");
 
-template <bool EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     scaled_mm_mx_pair_kernel(const __grid_constant__ CUtensorMap tma_a,
                              const __grid_constant__ CUtensorMap tma_b,
                              const __grid_constant__ CUtensorMap tma_sfa,
-                             const __grid_constant__ CUtensorMap tma_sfb, const GemmArgs g) {
+                             const __grid_constant__ CUtensorMap tma_sfb,
+                             const __grid_constant__ CUtensorMap tma_res,
+                             const __grid_constant__ CUtensorMap tma_out, const GemmArgs g) {
     using T = MxPairTile;
     constexpr int S = T::kStages;
     constexpr int BN = T::BN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * T::kStageStride);  // leader's are used
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::kBarrierOffset);  // leader's are used
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;       // [2]
     uint64_t* acc_empty = acc_full + 2;   // [2], the leader's: both CTAs' epilogue warps
@@ -1554,10 +1761,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);  // 4 epilogue warps in each CTA of the pair
+            mbar_init(&acc_empty[b], 2 * kPairEpiWarps);  // both CTAs'
         }
-        mbar_init(ovl_free, 8);
+        mbar_init(ovl_free, 8);  // the 4 warps that read those columns, in each CTA
         mbar_init(drained, 1);
+        T::Epi::init_barriers(smem + T::kEpiOffset);
         fence_mbar_init_cluster();
     }
     if (warp == 1) {
@@ -1649,42 +1857,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- epilogue (each CTA): its 128 accumulator rows; the 32 columns
-        // shared by the two buffers first
-        const int quarter = warp & 3;
+        // ---- epilogue (each CTA): its 128 accumulator rows.  The 32 columns
+        // that the two buffers share (the last of buffer 0, the first of
+        // buffer 1) lie in the chunk that one of the two groups reads first.
+        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, warp - 2, lane);
         const uint32_t leader_acc_empty[2] = {peer_smem(&acc_empty[0], 0),
                                               peer_smem(&acc_empty[1], 0)};
         const uint32_t leader_ovl_free = peer_smem(ovl_free, 0);
+        // buffer 0: columns 192.. and 64.. (group 1), 128.. and 0.. (group 0);
+        // buffer 1: 64.. and 192.., 0.. and 128..
+        int tm, tn;
+        grouped_tile(pair, tiles_m, tiles_n, tm, tn);
+        int row0 = tm * 256 + (int)rank * 128 + quarter * 32, n0 = tn * 256;
+        epi.ahead(row0, n0 + group * kChunk + 128);
         int j = 0;
         for (int t = pair; t < tiles; t += npairs, ++j) {
             const int buf = j & 1;
-            int tm, tn;
-            grouped_tile(t, tiles_m, tiles_n, tm, tn);
-            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256;
+            const bool more = t + npairs < tiles;
+            if (more) grouped_tile(t + npairs, tiles_m, tiles_n, tm, tn);
+            const int row_next = tm * 256 + (int)rank * 128 + quarter * 32, n_next = tn * 256;
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
             if (!__all_sync(0xFFFFFFFFu, have)) break;
             tc_fence_after_sync();
-            const int row = m0 + quarter * 32 + lane;
-            const uint32_t base = tmem + (buf ? T::kBuf1 : 0u) + ((uint32_t)(quarter * 32) << 16);
-            // the shared columns are the last 32 of buffer 0, the first of buffer 1
-            const int first = buf ? 0 : BN - 32;
-            for (int i = 0; i < BN / 32; ++i) {
-                const int c = (first + 32 * i) % BN;
-                float v[32];
-                tmem_load_32(base + (uint32_t)c, v);
-                if (i == 0) {
+            const uint32_t base =
+                tmem + (buf ? T::kBuf1 : 0u) + ((uint32_t)(quarter * 32) << 16);
+            const int c0 = group * kChunk + (buf ? 0 : 128), c1 = group * kChunk + (buf ? 128 : 0);
+            if (!epi.chunk(base + (uint32_t)c0, 1.0f, row0, n0 + c0, true, row0, n0 + c1, [&]() {
+                    if (group != (buf ? 0 : 1)) return;
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(leader_ovl_free);
-                }
-                const int n = n0 + c;
-                if (row >= g.M || n >= g.N) continue;
-                store_row_chunk<EPI>(g, v, 1.0f, row, n);  // g.b_scale is null: no scaling
-            }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_acc_empty[buf]);
+                }))
+                break;
+            // the next tile's first chunk is that of the other buffer
+            if (!epi.chunk(base + (uint32_t)c1, 1.0f, row0, n0 + c1, more, row_next,
+                           n_next + group * kChunk + (buf ? 128 : 0), [&]() {
+                               tc_fence_before_sync();
+                               __syncwarp();
+                               if (lane == 0) mbar_arrive_cluster(leader_acc_empty[buf]);
+                           }))
+                break;
+            row0 = row_next;
+            n0 = n_next;
         }
+        epi.finish();
     }
 
     tc_fence_before_sync();
@@ -1742,7 +1959,7 @@ cudaError_t launch_on_pairs(void (*kernel)(Params...), int64_t pairs, int smem_b
                             cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
     cfg.dynamicSmemBytes = smem_bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1761,7 +1978,7 @@ cudaError_t launch_on_pairs(void (*kernel)(Params...), int64_t pairs, int smem_b
 // programmatic dependent launch: the kernel's set-up may overlap the previous
 // kernel of the stream.
 template <class... Params, class... Args>
-cudaError_t launch_persistent_threads(void (*kernel)(Params...), unsigned ctas, int threads,
+cudaError_t launch_persistent(void (*kernel)(Params...), unsigned ctas, int threads,
                                       int smem_bytes, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, 1, 1);
@@ -1774,13 +1991,6 @@ cudaError_t launch_persistent_threads(void (*kernel)(Params...), unsigned ctas, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// The same with the GEMM kernels' kThreads threads per CTA.
-template <class... Params, class... Args>
-cudaError_t launch_persistent(void (*kernel)(Params...), unsigned ctas, int smem_bytes,
-                              cudaStream_t stream, Args... args) {
-    return launch_persistent_threads(kernel, ctas, kThreads, smem_bytes, stream, args...);
 }
 
 // A [rows, K] byte matrix, box of 128 bytes x box_rows rows, 128-byte swizzle;
@@ -1796,6 +2006,30 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int b
               elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
+}
+
+// The bf16 output or residual [M, N] in the epilogue's boxes (kChunk columns x
+// 32 rows, 128-byte swizzle).
+bool make_box_map(CUtensorMap* map, const void* base, const GemmArgs& g) {
+    EncodeTiled fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M};
+    const cuuint64_t strides[1] = {(cuuint64_t)g.N * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kChunk, 32};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box,
+              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// The epilogue's maps: the residual's is the output's where there is none (or
+// where it is the output), and then not read.
+bool make_epilogue_maps(CUtensorMap* res, CUtensorMap* out, const GemmArgs& g) {
+    if (!make_box_map(out, g.out, g)) return false;
+    if (g.residual != nullptr && g.residual != g.out) return make_box_map(res, g.residual, g);
+    *res = *out;
+    return true;
 }
 
 // Blocked scale codes of a [rows, K] operand as a 3-D array of 32-bit words:
@@ -1839,23 +2073,24 @@ bool make_maps(CUtensorMap* ma, CUtensorMap* mb, const GemmArgs& g, const void* 
     return make_map3(ma, a, g.M, g.K, arows, z) && make_map3(mb, b, g.N, g.K, brows, z);
 }
 
-template <int BN, int AROWS, int Z, bool EPI>
+template <int BN, int AROWS, int Z>
 cudaError_t launch_bn(const GemmArgs& g, const void* a, const void* b, int sm_count,
                       cudaStream_t stream) {
     using T = Tile<BN, AROWS, Z>;
-    CUtensorMap ma, mb;
-    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z)) return cudaErrorInvalidValue;
-    constexpr auto kernel = scaled_mm_kernel<BN, AROWS, Z, EPI>;
+    CUtensorMap ma, mb, mr, mo;
+    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z) || !make_epilogue_maps(&mr, &mo, g))
+        return cudaErrorInvalidValue;
+    constexpr auto kernel = scaled_mm_kernel<BN, AROWS, Z>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + BN - 1) / BN) * ((g.M + kBM - 1) / kBM);
     const unsigned grid = (unsigned)(tiles < sm_count ? tiles : sm_count);  // one CTA per SM
-    return launch_persistent(kernel, grid, T::kSmemBytes, stream, ma, mb, g);
+    return launch_persistent(kernel, grid, T::kThreadsPerCta, T::kSmemBytes, stream, ma, mb, mr, mo, g);
 }
 
 // sfa, sfb: the MX form's scale codes of a and b (the blocked order), else
 // null.
-template <int NA, int Z, bool MX, bool EPI>
+template <int NA, int Z, bool MX = false>
 cudaError_t launch_swap_pairk(const GemmArgs& g, const void* a, const void* b, int sm_count,
                               cudaStream_t stream, const uint8_t* sfa = nullptr,
                               const uint8_t* sfb = nullptr) {
@@ -1863,57 +2098,59 @@ cudaError_t launch_swap_pairk(const GemmArgs& g, const void* a, const void* b, i
     CUtensorMap mx, mw;
     if (!make_map3(&mx, a, g.M, g.K, NA, Z) || !make_map3(&mw, b, g.N, g.K, T::kWRows, Z))
         return cudaErrorInvalidValue;
-    constexpr auto kernel = scaled_mm_swap_pairk_kernel<NA, Z, MX, EPI>;
+    constexpr auto kernel = scaled_mm_swap_pairk_kernel<NA, Z, MX>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (g.N + T::kWRows - 1) / T::kWRows;
     const unsigned grid = (unsigned)(tiles < sm_count ? tiles : sm_count);
-    return launch_persistent_threads(kernel, grid, T::kThreadsPerCta, T::kSmemBytes, stream, mx,
-                                     mw, g, sfa, sfb);
+    return launch_persistent(kernel, grid, T::kThreadsPerCta, T::kSmemBytes, stream, mx, mw, g, sfa,
+                             sfb);
 }
 
-template <bool EPI>
 cudaError_t launch_pair(const GemmArgs& g, const void* a, const void* b, int sm_count,
                         cudaStream_t stream) {
     using T = PairTile;
-    CUtensorMap ma, mb;
-    if (!make_map(&ma, a, g.M, g.K, 128) || !make_map(&mb, b, g.N, g.K, 128))
+    CUtensorMap ma, mb, mr, mo;
+    if (!make_map(&ma, a, g.M, g.K, 128) || !make_map(&mb, b, g.N, g.K, 128) ||
+        !make_epilogue_maps(&mr, &mo, g))
         return cudaErrorInvalidValue;
-    const cudaError_t e = enable_dynamic_smem<scaled_mm_pair_kernel<EPI>>(T::kSmemBytes);
+    const cudaError_t e = enable_dynamic_smem<scaled_mm_pair_kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + 255) / 256) * ((g.M + 255) / 256);
     const int64_t pairs = tiles < sm_count / 2 ? tiles : sm_count / 2;
-    return launch_on_pairs(scaled_mm_pair_kernel<EPI>, pairs, T::kSmemBytes, stream, ma, mb, g);
+    return launch_on_pairs(scaled_mm_pair_kernel, pairs, T::kSmemBytes, stream, ma, mb, mr, mo, g);
 }
 
-template <int BN, int AROWS, int Z, bool EPI>
+template <int BN, int AROWS, int Z>
 cudaError_t launch_mx(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
                       const uint8_t* sfb, int sm_count, cudaStream_t stream) {
     using T = MxTile<BN, AROWS, Z>;
-    CUtensorMap ma, mb;
-    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z)) return cudaErrorInvalidValue;
-    constexpr auto kernel = scaled_mm_mx_kernel<BN, AROWS, Z, EPI>;
+    CUtensorMap ma, mb, mr, mo;
+    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z) || !make_epilogue_maps(&mr, &mo, g))
+        return cudaErrorInvalidValue;
+    constexpr auto kernel = scaled_mm_mx_kernel<BN, AROWS, Z>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + BN - 1) / BN) * ((g.M + kBM - 1) / kBM);
     const unsigned grid = (unsigned)(tiles < sm_count ? tiles : sm_count);
-    return launch_persistent(kernel, grid, T::kSmemBytes, stream, ma, mb, g, sfa, sfb);
+    return launch_persistent(kernel, grid, T::kThreadsPerCta, T::kSmemBytes, stream, ma, mb, mr, mo,
+                             g, sfa, sfb);
 }
 
-template <bool EPI>
 cudaError_t launch_mx_pair(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
                            const uint8_t* sfb, int sm_count, cudaStream_t stream) {
     using T = MxPairTile;
-    CUtensorMap ma, mb, msa, msb;
+    CUtensorMap ma, mb, msa, msb, mr, mo;
     if (!make_map(&ma, a, g.M, g.K, 128) || !make_map(&mb, b, g.N, g.K, 128) ||
-        !make_sf_map(&msa, sfa, g.M, g.K, 1) || !make_sf_map(&msb, sfb, g.N, g.K, 2))
+        !make_sf_map(&msa, sfa, g.M, g.K, 1) || !make_sf_map(&msb, sfb, g.N, g.K, 2) ||
+        !make_epilogue_maps(&mr, &mo, g))
         return cudaErrorInvalidValue;
-    const cudaError_t e = enable_dynamic_smem<scaled_mm_mx_pair_kernel<EPI>>(T::kSmemBytes);
+    const cudaError_t e = enable_dynamic_smem<scaled_mm_mx_pair_kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + 255) / 256) * ((g.M + 255) / 256);
     const int64_t pairs = tiles < sm_count / 2 ? tiles : sm_count / 2;
-    return launch_on_pairs(scaled_mm_mx_pair_kernel<EPI>, pairs, T::kSmemBytes, stream, ma, mb,
-                           msa, msb, g);
+    return launch_on_pairs(scaled_mm_mx_pair_kernel, pairs, T::kSmemBytes, stream, ma, mb, msa,
+                           msb, mr, mo, g);
 }
 
 }  // namespace
@@ -1973,59 +2210,37 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
     return tile(kGemmTile, kBM, 64, atoms ? 2 : 1);
 }
 
-namespace {
-
-template <bool EPI>
-cudaError_t dispatch_mx(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
-                        const uint8_t* sfb, int sm_count, cudaStream_t stream) {
-    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, true, sm_count);
-    if (p.kernel == kGemmPair) return launch_mx_pair<EPI>(g, a, b, sfa, sfb, sm_count, stream);
-    if (p.kernel == kGemmSwap) {
-        if (p.a_rows == 8)
-            return launch_swap_pairk<8, 4, true, EPI>(g, a, b, sm_count, stream, sfa, sfb);
-        if (p.a_rows == 16)
-            return launch_swap_pairk<16, 4, true, EPI>(g, a, b, sm_count, stream, sfa, sfb);
-        return launch_swap_pairk<32, 4, true, EPI>(g, a, b, sm_count, stream, sfa, sfb);
-    }
-    if (p.tile_n == 128) return launch_mx<128, kBM, 1, EPI>(g, a, b, sfa, sfb, sm_count, stream);
-    if (p.a_rows == 64) return launch_mx<64, 64, 4, EPI>(g, a, b, sfa, sfb, sm_count, stream);
-    return launch_mx<64, kBM, 2, EPI>(g, a, b, sfa, sfb, sm_count, stream);
-}
-
-template <bool EPI>
-cudaError_t dispatch(const GemmArgs& g, const void* a, const void* b, int sm_count,
-                     cudaStream_t stream) {
-    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, false, sm_count);
-    if (p.kernel == kGemmPair) return launch_pair<EPI>(g, a, b, sm_count, stream);
-    if (p.kernel == kGemmSwap) {
-        if (p.a_rows == 8) return launch_swap_pairk<8, 8, false, EPI>(g, a, b, sm_count, stream);
-        if (p.a_rows == 16) return launch_swap_pairk<16, 4, false, EPI>(g, a, b, sm_count, stream);
-        return launch_swap_pairk<32, 4, false, EPI>(g, a, b, sm_count, stream);
-    }
-    if (p.tile_n == 128) return launch_bn<128, kBM, 1, EPI>(g, a, b, sm_count, stream);
-    if (p.a_rows == 64)
-        return p.k_tiles_per_stage == 4 ? launch_bn<64, 64, 4, EPI>(g, a, b, sm_count, stream)
-                                        : launch_bn<64, 64, 1, EPI>(g, a, b, sm_count, stream);
-    return p.k_tiles_per_stage == 2 ? launch_bn<64, kBM, 2, EPI>(g, a, b, sm_count, stream)
-                                    : launch_bn<64, kBM, 1, EPI>(g, a, b, sm_count, stream);
-}
-
-}  // namespace
-
-// A call with neither activation nor residual is the plain product.
 cudaError_t launch_scaled_mm_mx(const GemmArgs& g, const void* a, const void* b,
                                 const uint8_t* sfa, const uint8_t* sfb, int sm_count,
                                 cudaStream_t stream) {
-    return g.act != RRF_ACT_NONE || g.residual != nullptr
-               ? dispatch_mx<true>(g, a, b, sfa, sfb, sm_count, stream)
-               : dispatch_mx<false>(g, a, b, sfa, sfb, sm_count, stream);
+    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, true, sm_count);
+    if (p.kernel == kGemmPair) return launch_mx_pair(g, a, b, sfa, sfb, sm_count, stream);
+    if (p.kernel == kGemmSwap) {
+        if (p.a_rows == 8) return launch_swap_pairk<8, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
+        if (p.a_rows == 16)
+            return launch_swap_pairk<16, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
+        return launch_swap_pairk<32, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
+    }
+    if (p.tile_n == 128) return launch_mx<128, kBM, 1>(g, a, b, sfa, sfb, sm_count, stream);
+    if (p.a_rows == 64) return launch_mx<64, 64, 4>(g, a, b, sfa, sfb, sm_count, stream);
+    return launch_mx<64, kBM, 2>(g, a, b, sfa, sfb, sm_count, stream);
 }
 
 cudaError_t launch_scaled_mm(const GemmArgs& g, const void* a, const void* b, int sm_count,
                              cudaStream_t stream) {
-    return g.act != RRF_ACT_NONE || g.residual != nullptr
-               ? dispatch<true>(g, a, b, sm_count, stream)
-               : dispatch<false>(g, a, b, sm_count, stream);
+    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, false, sm_count);
+    if (p.kernel == kGemmPair) return launch_pair(g, a, b, sm_count, stream);
+    if (p.kernel == kGemmSwap) {
+        if (p.a_rows == 8) return launch_swap_pairk<8, 8>(g, a, b, sm_count, stream);
+        if (p.a_rows == 16) return launch_swap_pairk<16, 4>(g, a, b, sm_count, stream);
+        return launch_swap_pairk<32, 4>(g, a, b, sm_count, stream);
+    }
+    if (p.tile_n == 128) return launch_bn<128, kBM, 1>(g, a, b, sm_count, stream);
+    if (p.a_rows == 64)
+        return p.k_tiles_per_stage == 4 ? launch_bn<64, 64, 4>(g, a, b, sm_count, stream)
+                                        : launch_bn<64, 64, 1>(g, a, b, sm_count, stream);
+    return p.k_tiles_per_stage == 2 ? launch_bn<64, kBM, 2>(g, a, b, sm_count, stream)
+                                    : launch_bn<64, kBM, 1>(g, a, b, sm_count, stream);
 }
 
 }  // namespace rrf
