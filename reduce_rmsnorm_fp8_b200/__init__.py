@@ -49,21 +49,30 @@ _EXPORTS = (
     "RRF_AR_STATIC_MAX_WORLD", "rrf_allreduce_rmsnorm_fp8_static_ptr",
     "rrf_plan_scaled_mm", "RRF_GEMM_KERNEL_PAIR", "RRF_GEMM_KERNEL_TILE",
     "RRF_GEMM_KERNEL_SWAP", "RRF_FLAG_NO_PREFETCH", "RRF_FLAG_PREFETCH", "rrf_plan_fused_ex",
-    "RRF_DEVICE_ERROR_BOUNDS", "RRF_DEVICE_ERROR_INDEX", "RRF_MAX_HEAD_DIM", "RrfKvCache",
-    "rope_table", "rrf_qk_norm_rope", "rrf_kv_cache_write_fp8", "rrf_kv_cache_read_fp8",
-    "rrf_qk_norm_rope_kv_cache_fp8", "rrf_scaled_mm_fp8_act", "rrf_scaled_mm_mxfp8_act",
-    "RRF_ACT_NONE", "RRF_ACT_RELU", "RRF_ACT_GELU", "RRF_ACT_GELU_TANH", "RRF_ACT_SILU",
+    "RRF_DEVICE_ERROR_BOUNDS", "RRF_DEVICE_ERROR_INDEX", "RRF_MAX_HEAD_DIM", "RRF_ACT_NONE",
+    "RRF_ACT_RELU", "RRF_ACT_GELU", "RRF_ACT_GELU_TANH", "RRF_ACT_SILU",
 )
 
-__all__ = list(_EXPORTS)
+# from layer.py
+_LAYER_EXPORTS = (
+    "RrfKvCache", "rope_table", "rrf_qk_norm_rope", "rrf_kv_cache_write_fp8",
+    "rrf_kv_cache_read_fp8", "rrf_qk_norm_rope_kv_cache_fp8", "rrf_scaled_mm_fp8_act",
+    "rrf_scaled_mm_mxfp8_act",
+)
+
+__all__ = list(_EXPORTS + _LAYER_EXPORTS)
 
 
 def __getattr__(name):
     if name in _EXPORTS:
         from . import _lib  # raises ImportError if librrf.so is missing
         return getattr(_lib, name)
+    if name in _LAYER_EXPORTS:
+        from . import layer
+        value = globals()[name] = getattr(layer, name)  # found at once the next time
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted(list(globals()) + list(_EXPORTS))
+    return sorted(set(globals()) | set(__all__))

@@ -146,6 +146,35 @@ lib.rrf_check_scaled_mm_args.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i6
 lib.rrf_plan_scaled_mm.restype = _int
 lib.rrf_plan_scaled_mm.argtypes = [_i64, _i64, _i64, _int, _int] + [ctypes.POINTER(_int)] * 4 + \
     [ctypes.POINTER(_i64)] * 2
+_mm_act_args = [_vp] * 5 + [_int, _vp, _vp] + [_i64] * 3
+for _name in ("rrf_scaled_mm_fp8_act", "rrf_scaled_mm_mxfp8_act"):
+    getattr(lib, _name).restype = _int
+    getattr(lib, _name).argtypes = _mm_act_args + [_vp]
+for _name in ("rrf_check_scaled_mm_act_args", "rrf_check_scaled_mm_mx_act_args"):
+    getattr(lib, _name).restype = _int
+    getattr(lib, _name).argtypes = _mm_act_args
+# the per-head and cache calls; the cache struct as its bytes (RrfKvCache's layout)
+_view = [_vp, _i64, _i64]
+_norm_args = [_vp, _vp, _f32, _f32, _vp, _i64, _i64]
+lib.rrf_qk_norm_rope.restype = _int
+lib.rrf_qk_norm_rope.argtypes = _view * 4 + _norm_args + [_int, _vp] + [_i64] * 4 + [_vp]
+lib.rrf_check_qk_norm_rope_args.restype = _int
+lib.rrf_check_qk_norm_rope_args.argtypes = _view * 4 + _norm_args + [_vp] + [_i64] * 4
+lib.rrf_check_kv_cache_write_args.restype = _int
+lib.rrf_check_kv_cache_write_args.argtypes = _view * 2 + [_vp, _f32, _vp] + [_i64] * 3
+lib.rrf_kv_cache_write_fp8.restype = _int
+lib.rrf_kv_cache_write_fp8.argtypes = lib.rrf_check_kv_cache_write_args.argtypes + [_vp]
+lib.rrf_qk_norm_rope_kv_cache_fp8.restype = _int
+lib.rrf_qk_norm_rope_kv_cache_fp8.argtypes = _view * 4 + _norm_args + \
+    [_int, _vp, _vp, _f32, _vp] + [_i64] * 4 + [_vp]
+lib.rrf_check_qk_norm_rope_kv_cache_args.restype = _int
+lib.rrf_check_qk_norm_rope_kv_cache_args.argtypes = _view * 4 + _norm_args + \
+    [_vp, _vp, _f32, _vp] + [_i64] * 4
+lib.rrf_check_kv_cache_read_args.restype = _int
+lib.rrf_check_kv_cache_read_args.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp] + \
+    [_i64] * 3
+lib.rrf_kv_cache_read_fp8.restype = _int
+lib.rrf_kv_cache_read_fp8.argtypes = lib.rrf_check_kv_cache_read_args.argtypes + [_vp]
 lib.rrf_device_error.restype = _int
 lib.rrf_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), _int]
 lib.rrf_version.restype = ctypes.c_char_p
@@ -595,295 +624,4 @@ def rrf_scaled_mm_mxfp8(a, sa, b, sb, bias=None, out=None):
             a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(),
             bias.data_ptr() if bias is not None else None, out.data_ptr(), M, N, K,
             _stream(dev)))
-    return out
-
-
-# ---------------------------------------- heads, rotation and the FP8 cache ---
-
-class RrfKvCache(ctypes.Structure):
-    """The C struct rrf_kv_cache."""
-    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp),
-                ("num_pages", _i64), ("page_size", _i64), ("code_strides", _i64 * 3),
-                ("scale_strides", _i64 * 3)]
-
-
-_i64x3 = _i64 * 3
-_cache_p = ctypes.POINTER(RrfKvCache)
-_view = [_vp, _i64, _i64]
-_norm_args = [_vp, _vp, _f32, _f32, _vp, _i64, _i64]
-lib.rrf_qk_norm_rope.restype = _int
-lib.rrf_qk_norm_rope.argtypes = _view * 4 + _norm_args + [_int, _vp] + [_i64] * 4 + [_vp]
-lib.rrf_check_qk_norm_rope_args.restype = _int
-lib.rrf_check_qk_norm_rope_args.argtypes = _view * 4 + _norm_args + [_vp] + [_i64] * 4
-lib.rrf_check_kv_cache_write_args.restype = _int
-lib.rrf_check_kv_cache_write_args.argtypes = _view * 2 + [_vp, _f32, _cache_p] + [_i64] * 3
-lib.rrf_kv_cache_write_fp8.restype = _int
-lib.rrf_kv_cache_write_fp8.argtypes = lib.rrf_check_kv_cache_write_args.argtypes + [_vp]
-lib.rrf_qk_norm_rope_kv_cache_fp8.restype = _int
-lib.rrf_qk_norm_rope_kv_cache_fp8.argtypes = _view * 4 + _norm_args + \
-    [_int, _vp, _vp, _f32, _cache_p] + [_i64] * 4 + [_vp]
-lib.rrf_check_qk_norm_rope_kv_cache_args.restype = _int
-lib.rrf_check_qk_norm_rope_kv_cache_args.argtypes = _view * 4 + _norm_args + \
-    [_vp, _vp, _f32, _cache_p] + [_i64] * 4
-lib.rrf_check_kv_cache_read_args.restype = _int
-lib.rrf_check_kv_cache_read_args.argtypes = [_cache_p, _vp, _i64, _i64, _vp, _i64, _vp, _vp] + \
-    [_i64] * 3
-lib.rrf_kv_cache_read_fp8.restype = _int
-lib.rrf_kv_cache_read_fp8.argtypes = lib.rrf_check_kv_cache_read_args.argtypes + [_vp]
-
-
-def _launch(index, fn, *args):
-    """fn(*args, stream) on device ``index`` and its current stream.  (The
-    device is switched only when it is another one, and the stream's handle is
-    taken without a stream object: a call of this kind takes about as long on
-    the host as its kernel on the GPU.)"""
-    cuda = _torch()._C
-    if cuda._cuda_getDevice() == index:
-        status = fn(*args, cuda._cuda_getCurrentRawStream(index))
-    else:
-        with _torch().cuda.device(index):
-            status = fn(*args, cuda._cuda_getCurrentRawStream(index))
-    if status != 0:
-        _raise_on(status)
-
-
-def _heads_view(x, name, index, tokens=None, dim=None, heads=None):
-    """(pointer, token stride, head stride) of bf16 [tokens, heads, dim]."""
-    if x.dtype is not _torch().bfloat16 or x.dim() != 3 or x.get_device() != index or index < 0:
-        raise ValueError(f"{name} must be a 3-D bf16 CUDA tensor on the inputs' device")
-    t, h, d = x.shape
-    token, head, value = x.stride()
-    if value != 1 or (tokens is not None and (t != tokens or d != dim)) or \
-            (heads is not None and h != heads):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with contiguous heads")
-    return x.data_ptr(), token, head
-
-
-def _vector(x, name, dtype, n, index):
-    if x.dtype is not dtype or x.numel() != n or x.get_device() != index or \
-            not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on the "
-                         "inputs' device")
-    return x.data_ptr()
-
-
-def _norm_pointers(q_gamma, k_gamma, cos_sin, positions, tokens, dim, index):
-    """(q_gamma, k_gamma, cos_sin, max_positions, rot_dim, positions)"""
-    torch = _torch()
-    qg = _vector(q_gamma, "q_gamma", torch.bfloat16, dim, index)
-    kg = _vector(k_gamma, "k_gamma", torch.bfloat16, dim, index)
-    if cos_sin is None:
-        return qg, kg, None, 0, 0, None
-    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or \
-            cos_sin.get_device() != index or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous float32 [max_positions, rot_dim] tensor")
-    if positions is None:
-        raise ValueError("a rotation needs positions")
-    rows, rot = cos_sin.shape
-    if rot == 0:
-        raise ValueError("cos_sin has no columns: pass None for the norm alone")
-    return qg, kg, cos_sin.data_ptr(), rows, rot, \
-        _vector(positions, "positions", torch.int64, tokens, index)
-
-
-def _kv_cache(k_cache, k_scales, v_cache, v_scales, heads, dim, index):
-    torch = _torch()
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    if k_cache.dtype is not f8 or v_cache.dtype is not f8 or k_scales.dtype is not f32 or \
-            v_scales.dtype is not f32:
-        raise ValueError("the cache holds float8_e4m3fn codes and float32 scales")
-    shape, strides, scale_strides = k_cache.shape, k_cache.stride(), k_scales.stride()
-    if len(shape) != 4 or shape[2] != heads or shape[3] != dim or v_cache.shape != shape or \
-            k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
-        raise ValueError("codes must be [pages, page_size, kv_heads, head_dim] and scales "
-                         "[pages, page_size, kv_heads]")
-    if v_cache.stride() != strides or v_scales.stride() != scale_strides or strides[3] != 1:
-        raise ValueError("keys and values need the same strides, and contiguous heads")
-    if not (k_cache.get_device() == v_cache.get_device() == k_scales.get_device() ==
-            v_scales.get_device() == index):
-        raise ValueError("the cache must be on the inputs' device")
-    return RrfKvCache(k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
-                      v_scales.data_ptr(), shape[0], shape[1], strides[:3], scale_strides)
-
-
-def rope_table(max_positions: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
-    """The cos_sin table of the plain rotation: angle p * theta^(-2i / rot_dim)
-    for position p and pair i, taken in float64 and rounded to float32 once;
-    [max_positions, rot_dim], cosines first.  Prepared once, not a step of a
-    call."""
-    torch = _torch()
-    if rot_dim <= 0 or rot_dim % 16:
-        raise ValueError("rot_dim must be a positive multiple of 16")
-    i = torch.arange(rot_dim // 2, device=device, dtype=torch.float64)
-    p = torch.arange(max_positions, device=device, dtype=torch.float64)
-    angle = p[:, None] * torch.pow(float(theta), -2.0 * i / rot_dim)
-    return torch.cat((angle.cos(), angle.sin()), dim=1).float()
-
-
-def rrf_qk_norm_rope(q, k, q_gamma, k_gamma, eps, weight_offset, cos_sin, positions,
-                     interleaved=False, q_out=None, k_out=None):
-    """RMS norm of every head with gamma + weight_offset, then the rotation of
-    its first cos_sin.shape[1] values (cos_sin None: the norm alone).  q, k:
-    bf16 [tokens, heads, head_dim] with any token and head strides (parts of a
-    projection's output); cos_sin: float32 [max_positions, rot_dim]
-    (rope_table); positions: int64 [tokens].  q_out, k_out: new contiguous
-    tensors if None; pass q and k for an update in place.  Returns (q_out,
-    k_out)."""
-    torch = _torch()
-    index = q.get_device()
-    qv = _heads_view(q, "q", index)
-    tokens, q_heads, dim = q.shape
-    kv = _heads_view(k, "k", index, tokens, dim)
-    norm = _norm_pointers(q_gamma, k_gamma, cos_sin, positions, tokens, dim, index)
-    if q_out is None:
-        q_out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=q.device)
-    if k_out is None:
-        k_out = torch.empty((tokens, k.shape[1], dim), dtype=torch.bfloat16, device=q.device)
-    _launch(index, lib.rrf_qk_norm_rope, *qv, *kv,
-            *_heads_view(q_out, "q_out", index, tokens, dim, q_heads),
-            *_heads_view(k_out, "k_out", index, tokens, dim, k.shape[1]), norm[0], norm[1], eps,
-            weight_offset, norm[2], norm[3], norm[4], bool(interleaved), norm[5], tokens, q_heads,
-            k.shape[1], dim)
-    return q_out, k_out
-
-
-def rrf_kv_cache_write_fp8(k, v, slots, k_cache, k_scales, v_cache, v_scales,
-                           scale_ub=float("inf")):
-    """Quantise keys and values, bf16 [tokens, kv_heads, head_dim], into slots
-    of a paged cache: one scale per token and head.  slots: int64 [tokens]
-    (page * page_size + place; negative: a padding token, not stored; the
-    others must differ).  k_cache, v_cache: float8_e4m3fn [pages, page_size,
-    kv_heads, head_dim]; k_scales, v_scales: float32 [pages, page_size,
-    kv_heads]; any strides that keep a head's codes contiguous, the same for
-    keys and values.  Updates the cache."""
-    index = k.get_device()
-    kv = _heads_view(k, "k", index)
-    tokens, heads, dim = k.shape
-    vv = _heads_view(v, "v", index, tokens, dim, heads)
-    cache = _kv_cache(k_cache, k_scales, v_cache, v_scales, heads, dim, index)
-    _launch(index, lib.rrf_kv_cache_write_fp8, *kv, *vv,
-            _vector(slots, "slots", _torch().int64, tokens, index), scale_ub, cache, tokens,
-            heads, dim)
-
-
-def rrf_qk_norm_rope_kv_cache_fp8(q, k, v, q_gamma, k_gamma, eps, weight_offset, cos_sin,
-                                  positions, slots, k_cache, k_scales, v_cache, v_scales,
-                                  scale_ub=float("inf"), interleaved=False, q_out=None):
-    """rrf_qk_norm_rope and rrf_kv_cache_write_fp8 in one pass: q normalised,
-    rotated and written to q_out (new if None; q for an update in place), k
-    normalised, rotated and quantised into its slots, v quantised into its
-    slots.  Returns q_out."""
-    torch = _torch()
-    index = q.get_device()
-    qv = _heads_view(q, "q", index)
-    tokens, q_heads, dim = q.shape
-    kv = _heads_view(k, "k", index, tokens, dim)
-    heads = k.shape[1]
-    vv = _heads_view(v, "v", index, tokens, dim, heads)
-    norm = _norm_pointers(q_gamma, k_gamma, cos_sin, positions, tokens, dim, index)
-    cache = _kv_cache(k_cache, k_scales, v_cache, v_scales, heads, dim, index)
-    if q_out is None:
-        q_out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=q.device)
-    _launch(index, lib.rrf_qk_norm_rope_kv_cache_fp8, *qv, *kv, *vv,
-            *_heads_view(q_out, "q_out", index, tokens, dim, q_heads), norm[0], norm[1], eps,
-            weight_offset, norm[2], norm[3], norm[4], bool(interleaved), norm[5],
-            _vector(slots, "slots", torch.int64, tokens, index), scale_ub, cache, tokens, q_heads,
-            heads, dim)
-    return q_out
-
-
-def rrf_kv_cache_read_fp8(k_cache, k_scales, v_cache, v_scales, block_table, seq_starts, k_out,
-                          v_out):
-    """Read a batch's keys and values back as bf16: row seq_starts[s] + t of
-    k_out and v_out (contiguous bf16 [rows, kv_heads, head_dim]) gets place
-    t % page_size of page block_table[s][t // page_size].  block_table: int32
-    [sequences, pages per sequence]; seq_starts: int32 [sequences + 1].  Rows
-    of no sequence stay as they are.  Returns (k_out, v_out)."""
-    torch = _torch()
-    index = k_out.get_device()
-    if k_out.dtype is not torch.bfloat16 or v_out.dtype is not torch.bfloat16 or \
-            k_out.dim() != 3 or k_out.shape != v_out.shape or not k_out.is_contiguous() or \
-            not v_out.is_contiguous() or v_out.get_device() != index or index < 0:
-        raise ValueError("k_out and v_out must be contiguous bf16 CUDA tensors of one shape, "
-                         "[rows, kv_heads, head_dim]")
-    rows, heads, dim = k_out.shape
-    cache = _kv_cache(k_cache, k_scales, v_cache, v_scales, heads, dim, index)
-    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or \
-            block_table.get_device() != index or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be an int32 [sequences, pages] tensor")
-    sequences, width = block_table.shape
-    _launch(index, lib.rrf_kv_cache_read_fp8, cache, block_table.data_ptr(),
-            block_table.stride(0), width,
-            _vector(seq_starts, "seq_starts", torch.int32, sequences + 1, index), sequences,
-            k_out.data_ptr(), v_out.data_ptr(), rows, heads, dim)
-    return k_out, v_out
-
-
-# ------------------------------------------- products with their epilogue ---
-
-_mm_act_args = [_vp] * 5 + [_int, _vp, _vp] + [_i64] * 3
-for _name in ("rrf_scaled_mm_fp8_act", "rrf_scaled_mm_mxfp8_act"):
-    getattr(lib, _name).restype = _int
-    getattr(lib, _name).argtypes = _mm_act_args + [_vp]
-for _name in ("rrf_check_scaled_mm_act_args", "rrf_check_scaled_mm_mx_act_args"):
-    getattr(lib, _name).restype = _int
-    getattr(lib, _name).argtypes = _mm_act_args
-
-_ACTIVATIONS = {None: RRF_ACT_NONE, "none": RRF_ACT_NONE, "relu": RRF_ACT_RELU,
-                "gelu": RRF_ACT_GELU, "gelu_tanh": RRF_ACT_GELU_TANH, "silu": RRF_ACT_SILU}
-
-
-def _mm_operands(a, b, bias, activation, residual, out):
-    """(index, M, N, K, activation code, out) of a checked product."""
-    torch = _torch()
-    index = a.get_device()
-    f8 = torch.float8_e4m3fn
-    if a.dtype is not f8 or b.dtype is not f8 or a.dim() != 2 or b.dim() != 2 or index < 0 or \
-            b.get_device() != index or not a.is_contiguous() or not b.is_contiguous():
-        raise ValueError("a and b must be contiguous 2-D float8_e4m3fn tensors on one CUDA device")
-    (m, k), (n, kb) = a.shape, b.shape
-    if kb != k:
-        raise ValueError("a and b need the same K")
-    if activation not in _ACTIVATIONS:
-        raise ValueError(f"activation must be one of {sorted(filter(None, _ACTIVATIONS))}")
-    bf16 = torch.bfloat16
-    if bias is not None:
-        _vector(bias, "bias", bf16, n, index)
-    for x, name in ((residual, "residual"), (out, "out")):
-        if x is not None and (x.dtype is not bf16 or x.shape != (m, n) or
-                              x.get_device() != index or not x.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous bf16 [{m}, {n}] tensor on a's device")
-    if out is None:
-        out = torch.empty((m, n), dtype=bf16, device=a.device)
-    return index, m, n, k, _ACTIVATIONS[activation], out
-
-
-def rrf_scaled_mm_fp8_act(a, a_scale, b, b_scale, bias=None, activation="none", residual=None,
-                          out=None):
-    """out = RN_bf16(act((a @ b^T) * a_scale * b_scale + bias) + residual):
-    rrf_scaled_mm_fp8 with the rest of a projection in its epilogue, rounded
-    once.  activation: "none", "relu", "gelu" (erf), "gelu_tanh" or "silu";
-    residual: bf16 [M, N] or None; pass it as out too for an update in place.
-    Returns out, bf16 [M, N]."""
-    index, m, n, k, act, out = _mm_operands(a, b, bias, activation, residual, out)
-    f32 = _torch().float32
-    _launch(index, lib.rrf_scaled_mm_fp8_act, a.data_ptr(),
-            _vector(a_scale, "a_scale", f32, m, index), b.data_ptr(),
-            _vector(b_scale, "b_scale", f32, n, index),
-            None if bias is None else bias.data_ptr(), act,
-            None if residual is None else residual.data_ptr(), out.data_ptr(), m, n, k)
-    return out
-
-
-def rrf_scaled_mm_mxfp8_act(a, sa, b, sb, bias=None, activation="none", residual=None, out=None):
-    """rrf_scaled_mm_mxfp8 with the epilogue of rrf_scaled_mm_fp8_act: sa and
-    sb are E8M0 scale codes in the blocked order.  Returns out, bf16 [M, N]."""
-    index, m, n, k, act, out = _mm_operands(a, b, bias, activation, residual, out)
-    u8 = _torch().uint8
-    _launch(index, lib.rrf_scaled_mm_mxfp8_act, a.data_ptr(),
-            _vector(sa, "sa", u8, mx_blocked_bytes(m, k), index), b.data_ptr(),
-            _vector(sb, "sb", u8, mx_blocked_bytes(n, k), index),
-            None if bias is None else bias.data_ptr(), act,
-            None if residual is None else residual.data_ptr(), out.data_ptr(), m, n, k)
     return out

@@ -2,10 +2,12 @@
 
     python -m reduce_rmsnorm_fp8_b200.build [--force] [--verbose] [--debug]
 
-Every translation unit under ``csrc/`` is compiled by nvcc for
+Every CUDA translation unit under ``csrc/`` is compiled by nvcc for
 ``-gencode arch=compute_100a,code=sm_100a`` (the fused kernel once per input
 bound, in parallel) and linked into ``reduce_rmsnorm_fp8_b200/librrf.so``
-with the CUDA runtime linked statically.  No GPU is needed to build.
+with the CUDA runtime linked statically.  ``csrc/rrf_torch.cpp``, the Python
+binding of layer.py's calls, is compiled by g++ against the installed torch
+into ``reduce_rmsnorm_fp8_b200/_rrf_torch.so``.  No GPU is needed to build.
 
 ``--debug`` builds the bounds-checking variant, ``librrf_debug.so`` (the same
 sources with RRF_DEBUG defined: every kernel checks the indices of its global
@@ -27,6 +29,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librrf.so")
+TORCH_SRC = os.path.join(CSRC, "rrf_torch.cpp")
+TORCH_LIB = os.path.join(PKG, "_rrf_torch.so")
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB = os.path.join(PKG, "librrf_debug.so")
 
@@ -61,11 +65,40 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs() + [__file__])
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile _rrf_torch.so unless it is newer than its sources and torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inputs = [TORCH_SRC, os.path.join(INCLUDE, "rrf.h"), __file__, torch.version.__file__]
+    if not force and os.path.exists(TORCH_LIB) and \
+            os.path.getmtime(TORCH_LIB) > max(os.path.getmtime(p) for p in inputs):
+        return TORCH_LIB
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    for d in (os.path.join(root, "include"),
+              os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
+              sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", d]
+    cmd += [TORCH_SRC, "-o", tmp, "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on rrf_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile and link librrf.so (debug: librrf_debug.so, the bounds-checking
-    build) unless it is newer than every source."""
+    build) unless it is newer than every source, and the Python binding."""
     lib_path, build_dir = (DEBUG_LIB, DEBUG_BUILD_DIR) if debug else (LIB, BUILD_DIR)
+    binding = concurrent.futures.ThreadPoolExecutor(max_workers=1).submit(build_binding, force)
     if not force and not stale(lib_path):
+        binding.result()
         return lib_path
     os.makedirs(build_dir, exist_ok=True)
     cc = nvcc()
@@ -94,6 +127,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
+    binding.result()
     return lib_path
 
 

@@ -39,7 +39,8 @@ def cache_struct(rrf, pages=4, page=16, heads=HK, dim=D, codes=None, scales=None
              code_strides=codes or (page * heads * dim, heads * dim, dim),
              scale_strides=scales or (page * heads, heads, 1))
     c.update(change)
-    return rrf.RrfKvCache(*[tuple(v) if isinstance(v, (tuple, list)) else v for v in c.values()])
+    return bytes(rrf.RrfKvCache(*[tuple(v) if isinstance(v, (tuple, list)) else v
+                                  for v in c.values()]))
 
 
 def status(rrf, n):
