@@ -538,8 +538,8 @@ rrf_status rrf_check_scaled_mm_args(const void* a, const float* a_scale, const v
  * activation  one of RRF_ACT_*
  * residual    bf16 [M, N] or NULL, 16-byte aligned; it may be out (the update
  *             in place) but not overlap it otherwise
- * The other arguments, the shapes and the kernels (rrf_plan_scaled_mm) are
- * those of rrf_scaled_mm_fp8 and rrf_scaled_mm_mxfp8.
+ * The other arguments and the shapes are those of rrf_scaled_mm_fp8 and
+ * rrf_scaled_mm_mxfp8; the kernel is rrf_plan_scaled_mm_act's.
  * Errors: as theirs, and RRF_ERR_VALUE (activation). */
 rrf_status rrf_scaled_mm_fp8_act(const void* a, const float* a_scale, const void* b,
                                  const float* b_scale, const void* bias, int activation,
@@ -567,6 +567,13 @@ rrf_status rrf_check_scaled_mm_mx_act_args(const void* a, const void* sa, const 
 #define RRF_GEMM_KERNEL_SWAP 3 /* operands swapped, 64 weight rows of each of two
                                   k-tiles on the MMA's M side, the call's rows padded
                                   to a_rows (per-token and MX, at most 32 rows)       */
+
+/* rrf_plan_scaled_mm_act -- as rrf_plan_scaled_mm, below, for
+ * rrf_scaled_mm_fp8_act (mx == 0) and rrf_scaled_mm_mxfp8_act (mx != 0): the
+ * same kernels, chosen by the measured time of a round of tiles. */
+rrf_status rrf_plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, int mx, int sm_count,
+                                  int* kernel, int* a_rows, int* tile_n, int* k_tiles_per_stage,
+                                  int64_t* tiles, int64_t* ctas);
 
 /* rrf_plan_scaled_mm -- the kernel rrf_scaled_mm_fp8 (mx == 0) or
  * rrf_scaled_mm_mxfp8 (mx != 0) runs for an M x N x K product on a GPU with

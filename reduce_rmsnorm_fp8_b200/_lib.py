@@ -143,6 +143,9 @@ lib.rrf_scaled_mm_fp8.restype = _int
 lib.rrf_scaled_mm_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]
 lib.rrf_check_scaled_mm_args.restype = _int
 lib.rrf_check_scaled_mm_args.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64]
+lib.rrf_plan_scaled_mm_act.restype = _int
+lib.rrf_plan_scaled_mm_act.argtypes = [_i64, _i64, _i64, _int, _int] + \
+    [ctypes.POINTER(_int)] * 4 + [ctypes.POINTER(_i64)] * 2
 lib.rrf_plan_scaled_mm.restype = _int
 lib.rrf_plan_scaled_mm.argtypes = [_i64, _i64, _i64, _int, _int] + [ctypes.POINTER(_int)] * 4 + \
     [ctypes.POINTER(_i64)] * 2
@@ -545,10 +548,18 @@ def rrf_check_scaled_mm_args(a, a_scale, b, b_scale, bias, out, M, N, K) -> int:
 def rrf_plan_scaled_mm(M: int, N: int, K: int, sm_count: int, mx: bool = False) -> dict:
     """The GEMM kernel rrf_scaled_mm_fp8 (or, mx=True, rrf_scaled_mm_mxfp8)
     runs for an M x N x K product on sm_count SMs (host only)."""
+    return _plan_scaled_mm(lib.rrf_plan_scaled_mm, M, N, K, sm_count, mx)
+
+
+def rrf_plan_scaled_mm_act(M: int, N: int, K: int, sm_count: int, mx: bool = False) -> dict:
+    """The same for rrf_scaled_mm_fp8_act and rrf_scaled_mm_mxfp8_act."""
+    return _plan_scaled_mm(lib.rrf_plan_scaled_mm_act, M, N, K, sm_count, mx)
+
+
+def _plan_scaled_mm(plan, M, N, K, sm_count, mx):
     ints = [_int() for _ in range(4)]
     longs = [_i64() for _ in range(2)]
-    _raise_on(lib.rrf_plan_scaled_mm(M, N, K, int(bool(mx)), sm_count,
-                                     *[ctypes.byref(o) for o in ints + longs]))
+    _raise_on(plan(M, N, K, int(bool(mx)), sm_count, *[ctypes.byref(o) for o in ints + longs]))
     names = {RRF_GEMM_KERNEL_PAIR: "pair", RRF_GEMM_KERNEL_TILE: "tile",
              RRF_GEMM_KERNEL_SWAP: "swap"}
     return {"kernel": names.get(ints[0].value), "a_rows": ints[1].value,

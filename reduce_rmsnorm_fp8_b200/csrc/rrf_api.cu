@@ -944,14 +944,12 @@ extern "C" rrf_status rrf_check_scaled_mm_act_args(const void* a, const float* a
     return st != RRF_OK ? st : check_epilogue(activation, residual, out, M, N);
 }
 
-extern "C" rrf_status rrf_scaled_mm_fp8_act(const void* a, const float* a_scale, const void* b,
-                                            const float* b_scale, const void* bias,
-                                            int activation, const void* residual, void* out,
-                                            int64_t M, int64_t N, int64_t K,
-                                            rrf_stream_t stream) {
-    rrf_status st = rrf_check_scaled_mm_act_args(a, a_scale, b, b_scale, bias, activation,
-                                                 residual, out, M, N, K);
-    if (st != RRF_OK || M == 0) return st;
+// Checked products (activation may be kPlainProduct).
+static rrf_status run_scaled_mm(const void* a, const float* a_scale, const void* b,
+                                const float* b_scale, const void* bias, int activation,
+                                const void* residual, void* out, int64_t M, int64_t N, int64_t K,
+                                rrf_stream_t stream) {
+    rrf_status st;
     int sm_count = 0;
     if ((st = current_sm_count(&sm_count)) != RRF_OK) return st;
     unsigned int* err = nullptr;
@@ -973,17 +971,29 @@ extern "C" rrf_status rrf_scaled_mm_fp8_act(const void* a, const float* a_scale,
     return e == cudaSuccess ? RRF_OK : cuda_fail(e);
 }
 
+extern "C" rrf_status rrf_scaled_mm_fp8_act(const void* a, const float* a_scale, const void* b,
+                                            const float* b_scale, const void* bias,
+                                            int activation, const void* residual, void* out,
+                                            int64_t M, int64_t N, int64_t K,
+                                            rrf_stream_t stream) {
+    const rrf_status st = rrf_check_scaled_mm_act_args(a, a_scale, b, b_scale, bias, activation,
+                                                       residual, out, M, N, K);
+    if (st != RRF_OK || M == 0) return st;
+    return run_scaled_mm(a, a_scale, b, b_scale, bias, activation, residual, out, M, N, K, stream);
+}
+
 extern "C" rrf_status rrf_scaled_mm_fp8(const void* a, const float* a_scale, const void* b,
                                         const float* b_scale, const void* bias, void* out,
                                         int64_t M, int64_t N, int64_t K, rrf_stream_t stream) {
-    return rrf_scaled_mm_fp8_act(a, a_scale, b, b_scale, bias, RRF_ACT_NONE, nullptr, out, M, N,
-                                 K, stream);
+    const rrf_status st = rrf_check_scaled_mm_args(a, a_scale, b, b_scale, bias, out, M, N, K);
+    if (st != RRF_OK || M == 0) return st;
+    return run_scaled_mm(a, a_scale, b, b_scale, bias, kPlainProduct, nullptr, out, M, N, K,
+                         stream);
 }
 
-extern "C" rrf_status rrf_plan_scaled_mm(int64_t M, int64_t N, int64_t K, int mx, int sm_count,
-                                         int* kernel, int* a_rows, int* tile_n,
-                                         int* k_tiles_per_stage, int64_t* tiles,
-                                         int64_t* ctas) {
+static rrf_status plan_query(bool act, int64_t M, int64_t N, int64_t K, int mx, int sm_count,
+                             int* kernel, int* a_rows, int* tile_n, int* k_tiles_per_stage,
+                             int64_t* tiles, int64_t* ctas) {
     if (!kernel || !a_rows || !tile_n || !k_tiles_per_stage || !tiles || !ctas)
         return RRF_ERR_NULL;
     // the calls' own shape rules, checked without operands
@@ -998,7 +1008,8 @@ extern "C" rrf_status rrf_plan_scaled_mm(int64_t M, int64_t N, int64_t K, int mx
         *tiles = *ctas = 0;
         return RRF_OK;
     }
-    const GemmPlan p = plan_scaled_mm(M, N, K, mx != 0, sm_count);
+    const GemmPlan p = act ? plan_scaled_mm_act(M, N, K, mx != 0, sm_count)
+                           : plan_scaled_mm(M, N, K, mx != 0, sm_count);
     *kernel = p.kernel;
     *a_rows = p.a_rows;
     *tile_n = p.tile_n;
@@ -1006,6 +1017,22 @@ extern "C" rrf_status rrf_plan_scaled_mm(int64_t M, int64_t N, int64_t K, int mx
     *tiles = p.tiles;
     *ctas = p.ctas;
     return RRF_OK;
+}
+
+extern "C" rrf_status rrf_plan_scaled_mm(int64_t M, int64_t N, int64_t K, int mx, int sm_count,
+                                         int* kernel, int* a_rows, int* tile_n,
+                                         int* k_tiles_per_stage, int64_t* tiles,
+                                         int64_t* ctas) {
+    return plan_query(false, M, N, K, mx, sm_count, kernel, a_rows, tile_n, k_tiles_per_stage,
+                      tiles, ctas);
+}
+
+extern "C" rrf_status rrf_plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, int mx,
+                                             int sm_count, int* kernel, int* a_rows, int* tile_n,
+                                             int* k_tiles_per_stage, int64_t* tiles,
+                                             int64_t* ctas) {
+    return plan_query(true, M, N, K, mx, sm_count, kernel, a_rows, tile_n, k_tiles_per_stage,
+                      tiles, ctas);
 }
 
 extern "C" rrf_status rrf_check_scaled_mm_mx_args(const void* a, const void* sa,
@@ -1039,13 +1066,11 @@ extern "C" rrf_status rrf_check_scaled_mm_mx_act_args(const void* a, const void*
     return st != RRF_OK ? st : check_epilogue(activation, residual, out, M, N);
 }
 
-extern "C" rrf_status rrf_scaled_mm_mxfp8_act(const void* a, const void* sa, const void* b,
-                                              const void* sb, const void* bias, int activation,
-                                              const void* residual, void* out, int64_t M,
-                                              int64_t N, int64_t K, rrf_stream_t stream) {
-    rrf_status st = rrf_check_scaled_mm_mx_act_args(a, sa, b, sb, bias, activation, residual, out,
-                                                    M, N, K);
-    if (st != RRF_OK || M == 0) return st;
+static rrf_status run_scaled_mm_mx(const void* a, const void* sa, const void* b, const void* sb,
+                                   const void* bias, int activation, const void* residual,
+                                   void* out, int64_t M, int64_t N, int64_t K,
+                                   rrf_stream_t stream) {
+    rrf_status st;
     int sm_count = 0;
     if ((st = current_sm_count(&sm_count)) != RRF_OK) return st;
     unsigned int* err = nullptr;
@@ -1067,11 +1092,22 @@ extern "C" rrf_status rrf_scaled_mm_mxfp8_act(const void* a, const void* sa, con
     return e == cudaSuccess ? RRF_OK : cuda_fail(e);
 }
 
+extern "C" rrf_status rrf_scaled_mm_mxfp8_act(const void* a, const void* sa, const void* b,
+                                              const void* sb, const void* bias, int activation,
+                                              const void* residual, void* out, int64_t M,
+                                              int64_t N, int64_t K, rrf_stream_t stream) {
+    const rrf_status st = rrf_check_scaled_mm_mx_act_args(a, sa, b, sb, bias, activation,
+                                                          residual, out, M, N, K);
+    if (st != RRF_OK || M == 0) return st;
+    return run_scaled_mm_mx(a, sa, b, sb, bias, activation, residual, out, M, N, K, stream);
+}
+
 extern "C" rrf_status rrf_scaled_mm_mxfp8(const void* a, const void* sa, const void* b,
                                           const void* sb, const void* bias, void* out, int64_t M,
                                           int64_t N, int64_t K, rrf_stream_t stream) {
-    return rrf_scaled_mm_mxfp8_act(a, sa, b, sb, bias, RRF_ACT_NONE, nullptr, out, M, N, K,
-                                   stream);
+    const rrf_status st = rrf_check_scaled_mm_mx_args(a, sa, b, sb, bias, out, M, N, K);
+    if (st != RRF_OK || M == 0) return st;
+    return run_scaled_mm_mx(a, sa, b, sb, bias, kPlainProduct, nullptr, out, M, N, K, stream);
 }
 
 // ------------------------------------------- heads and the FP8 cache ---

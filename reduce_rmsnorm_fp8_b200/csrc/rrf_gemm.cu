@@ -266,7 +266,7 @@ __device__ __forceinline__ void activate_pairs(float2 y[PAIRS]) {
 // (one branch for all the values)
 template <int PAIRS>
 __device__ __forceinline__ void activate_all(int act, float2 y[PAIRS]) {
-    if (act == RRF_ACT_NONE) return;
+    if (act <= RRF_ACT_NONE) return;
     if (act == RRF_ACT_RELU) activate_pairs<RRF_ACT_RELU, PAIRS>(y);
     else if (act == RRF_ACT_SILU) activate_pairs<RRF_ACT_SILU, PAIRS>(y);
     else if (act == RRF_ACT_GELU) activate_pairs<RRF_ACT_GELU, PAIRS>(y);
@@ -475,7 +475,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // which needs K % 128 == 0 (k-atoms past K read as zero).
 template <int BN, int AROWS, int Z>
 struct Tile {
-    static_assert(AROWS == kBM || (AROWS <= 64 && AROWS % 8 == 0 && BN == 64),
+    static_assert(AROWS == kBM || (AROWS <= 64 && AROWS % 8 == 0),
                   "the MMA's 128 rows of A must stay inside the stage");
     static_assert((Z - 1) * AROWS * kBK + kBM * kBK <= Z * (AROWS + BN) * kBK,
                   "the MMA's 128 rows of A must stay inside the stage");
@@ -488,7 +488,10 @@ struct Tile {
     static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
     // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 8
     // at 64, 12 with 64-row A stages, 3 with four k-tiles of 64 rows
-    using Epi = EpiWarp<kEpiWarps, 1, true>;
+    // with 64-row A stages only the first two quarters of the accumulator
+    // hold rows, and only their warps have boxes
+    static constexpr int kEpiAreas = AROWS == kBM || BN == kChunk ? kEpiWarps : kEpiWarps / 2;
+    using Epi = EpiWarp<kEpiAreas, 1, true>;
     static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
     static constexpr int kStages = kBudget / kStageBytes > 12 ? 12 : kBudget / kStageBytes;
     static constexpr int kTmemCols = 2 * BN;  // two accumulators
@@ -653,7 +656,8 @@ __global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
         // ---- epilogue: warp w reads accumulator lanes 32 * (w % 4) ... and
         // 64 columns
         const int quarter = warp & 3, c = ((warp - 2) >> 2) * kChunk;
-        typename T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, warp - 2, lane);
+        const int area = T::kEpiAreas == T::kEpiWarps ? warp - 2 : 2 * (c / kChunk) + (quarter & 1);
+        typename T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, area, lane);
         int row0 = (blockIdx.x / tiles_n) * kBM + quarter * 32, n = (blockIdx.x % tiles_n) * BN + c;
         epi.ahead(row0, n);
         int j = 0;
@@ -1449,7 +1453,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 template <int BN, int AROWS, int Z>
 struct MxTile {
     static_assert(BN == 128 || BN == 64, "one scale atom covers 128 columns");
-    static_assert(AROWS == kBM || (AROWS <= 64 && AROWS % 8 == 0 && BN == 64),
+    static_assert(AROWS == kBM || (AROWS <= 64 && AROWS % 8 == 0),
                   "the MMA's 128 rows of A must stay inside the stage");
     static_assert((Z - 1) * AROWS * kBK + kBM * kBK <= Z * (AROWS + BN) * kBK,
                   "the MMA's 128 rows of A must stay inside the stage");
@@ -1465,7 +1469,8 @@ struct MxTile {
     static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
     // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 4
     // at 64, 3 with four 64-row k-tiles
-    using Epi = EpiWarp<kEpiWarps, 1, false>;
+    static constexpr int kEpiAreas = AROWS == kBM || BN == kChunk ? kEpiWarps : kEpiWarps / 2;
+    using Epi = EpiWarp<kEpiAreas, 1, false>;
     static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
     static constexpr int kStages = kBudget / kStageStride > 12 ? 12 : kBudget / kStageStride;
     static constexpr int kAccCols = 2 * BN;          // two accumulators
@@ -1613,7 +1618,8 @@ __global__ void __launch_bounds__(MxTile<BN, AROWS, Z>::kThreadsPerCta, 1)
     } else {
         // ---- epilogue: the scales are inside the accumulator
         const int quarter = warp & 3, c = ((warp - 2) >> 2) * kChunk;
-        typename T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, warp - 2, lane);
+        const int area = T::kEpiAreas == T::kEpiWarps ? warp - 2 : 2 * (c / kChunk) + (quarter & 1);
+        typename T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, area, lane);
         int row0 = (blockIdx.x / tiles_n) * kBM + quarter * 32, n = (blockIdx.x % tiles_n) * BN + c;
         epi.ahead(row0, n);
         int j = 0;
@@ -2210,10 +2216,60 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
     return tile(kGemmTile, kBM, 64, atoms ? 2 : 1);
 }
 
+// The products with an epilogue.  A persistent CTA (or pair) takes its tiles
+// in rounds, and a round's time is near a fixed part e plus the k-tiles times
+// c, whatever M and N.  Measured on B200 (us; N = 1024 .. 16384, M = 48 ..
+// 4096, K = 1024 and 4096, silu and residual):
+//   64 columns, 64-row A stages      e 0.3  c 0.24    (K % 128 != 0: c 0.35)
+//   64 columns, 128 rows             e 0.7  c 0.254   (K % 128 != 0: c 0.35)
+//   128 columns, 64-row A stages     e 1.5  c 0.26
+//   128 columns, 128 rows            e 2.0  c 0.2875
+//   256 x 256 on SM pairs            e 5.0  c 0.29
+// (the operands that a CTA loads per k-tile count, hardly its products: 64
+// columns cost nearly as much as 128).  The kernel of the least rounds * (e +
+// k-tiles * c) is taken; at most 32 rows stay with the swapped kernel.
+// Against plan_scaled_mm's choice: 512 x 7168 x 4096 22.9 (pairs) for 27.1 us,
+// 256 x 7168 x 4096 16.7 (128 columns) for 21.6, 64 x 16384 x 7168 25.8 (128
+// columns) for 31.3, MX 1999 x 2576 x 1024 15.6 (128 columns) for 18.1.
+GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) {
+    GemmPlan best = plan_scaled_mm(M, N, K, mx, sm_count);
+    if (best.kernel == kGemmSwap) return best;
+    const bool atoms = K % kBK == 0;  // several k-tiles per box
+    const double ktiles = (double)((K + kBK - 1) / kBK);
+    double least = 0.0;
+    auto offer = [&](int kernel, int arows, int bn, int z, double e, double c) {
+        GemmPlan p;
+        p.kernel = kernel;
+        p.a_rows = arows;
+        p.tile_n = bn;
+        p.k_tiles_per_stage = z;
+        const int rows = kernel == kGemmPair ? 256 : kBM;
+        const int64_t units = kernel == kGemmPair ? sm_count / 2 : sm_count;
+        p.tiles = ((M + rows - 1) / rows) * ((N + bn - 1) / bn);
+        p.ctas = (p.tiles < units ? p.tiles : units) * (kernel == kGemmPair ? 2 : 1);
+        const double cost = (double)((p.tiles + units - 1) / units) * (e + ktiles * c);
+        if (least == 0.0 || cost < least) {
+            least = cost;
+            best = p;
+        }
+    };
+    if (M <= 64) {
+        offer(kGemmTile, 64, 64, atoms ? 4 : 1, 0.3, atoms ? 0.24 : 0.35);
+        if (atoms) offer(kGemmTile, 64, 128, 2, 1.5, 0.26);
+    }
+    if (M > 64 || !atoms) {
+        if (M > 64) offer(kGemmTile, kBM, 64, atoms ? 2 : 1, 0.7, atoms ? 0.254 : 0.35);
+        offer(kGemmTile, kBM, 128, 1, 2.0, 0.2875);
+    }
+    if (M > 128) offer(kGemmPair, 256, 256, 1, 5.0, 0.29);
+    return best;
+}
+
 cudaError_t launch_scaled_mm_mx(const GemmArgs& g, const void* a, const void* b,
                                 const uint8_t* sfa, const uint8_t* sfb, int sm_count,
                                 cudaStream_t stream) {
-    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, true, sm_count);
+    const GemmPlan p = g.act == kPlainProduct ? plan_scaled_mm(g.M, g.N, g.K, true, sm_count)
+                                 : plan_scaled_mm_act(g.M, g.N, g.K, true, sm_count);
     if (p.kernel == kGemmPair) return launch_mx_pair(g, a, b, sfa, sfb, sm_count, stream);
     if (p.kernel == kGemmSwap) {
         if (p.a_rows == 8) return launch_swap_pairk<8, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
@@ -2221,6 +2277,8 @@ cudaError_t launch_scaled_mm_mx(const GemmArgs& g, const void* a, const void* b,
             return launch_swap_pairk<16, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
         return launch_swap_pairk<32, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
     }
+    if (p.tile_n == 128 && p.a_rows == 64)
+        return launch_mx<128, 64, 2>(g, a, b, sfa, sfb, sm_count, stream);
     if (p.tile_n == 128) return launch_mx<128, kBM, 1>(g, a, b, sfa, sfb, sm_count, stream);
     if (p.a_rows == 64) return launch_mx<64, 64, 4>(g, a, b, sfa, sfb, sm_count, stream);
     return launch_mx<64, kBM, 2>(g, a, b, sfa, sfb, sm_count, stream);
@@ -2228,13 +2286,15 @@ cudaError_t launch_scaled_mm_mx(const GemmArgs& g, const void* a, const void* b,
 
 cudaError_t launch_scaled_mm(const GemmArgs& g, const void* a, const void* b, int sm_count,
                              cudaStream_t stream) {
-    const GemmPlan p = plan_scaled_mm(g.M, g.N, g.K, false, sm_count);
+    const GemmPlan p = g.act == kPlainProduct ? plan_scaled_mm(g.M, g.N, g.K, false, sm_count)
+                                 : plan_scaled_mm_act(g.M, g.N, g.K, false, sm_count);
     if (p.kernel == kGemmPair) return launch_pair(g, a, b, sm_count, stream);
     if (p.kernel == kGemmSwap) {
         if (p.a_rows == 8) return launch_swap_pairk<8, 8>(g, a, b, sm_count, stream);
         if (p.a_rows == 16) return launch_swap_pairk<16, 4>(g, a, b, sm_count, stream);
         return launch_swap_pairk<32, 4>(g, a, b, sm_count, stream);
     }
+    if (p.tile_n == 128 && p.a_rows == 64) return launch_bn<128, 64, 2>(g, a, b, sm_count, stream);
     if (p.tile_n == 128) return launch_bn<128, kBM, 1>(g, a, b, sm_count, stream);
     if (p.a_rows == 64)
         return p.k_tiles_per_stage == 4 ? launch_bn<64, 64, 4>(g, a, b, sm_count, stream)

@@ -73,15 +73,14 @@ __device__ __forceinline__ float fast_reciprocal(float v) {
 }
 
 // The codes of x[16] under m, their clamped maximum, and the row's scale.
-// EXACT, for values that are bf16: with a bf16 m, x / scale = 448 x / m is
-// often exactly a midpoint of the e4m3 grid, and a product with a rounded
-// reciprocal would land on either side of it.  So the quotient of n = 448 x
-// (exact) is corrected once by its exact remainder (Markstein's final step,
-// y + (n - y m) / m), which makes a representable quotient exact.  Values
-// that were computed in fp32 have no such midpoints and take the product.
+// For values that are bf16, x / scale = 448 x / m is often exactly a midpoint
+// of the e4m3 grid, and a product with a rounded reciprocal would land on
+// either side of it.  So the quotient of n = 448 x (exact then) is corrected
+// once by its exact remainder (Markstein's final step, y + (n - y m) / m),
+// which makes a representable quotient exact and any other one correct to
+// about half an ulp.
 // Rows above 1e30 are scaled by 2^-64 first, so that 448 x stays finite, and
 // values beyond a clamped maximum are cut to it (they saturate).
-template <bool EXACT>
 __device__ __forceinline__ float quantise(float2 x[8], float m, bool clamped, uint2& qa,
                                           uint2& qb) {
     if (clamped) {
@@ -98,7 +97,7 @@ __device__ __forceinline__ float quantise(float2 x[8], float m, bool clamped, ui
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(x[i], k2);
     // (an infinite scale: finite values are 0, infinities NaN)
-    if (EXACT && d < __int_as_float(0x7F800000)) {
+    if (d < __int_as_float(0x7F800000)) {
         const float2 minus_d = make_float2(-d, -d), f2 = make_float2(f, f);
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
@@ -296,9 +295,9 @@ __device__ __forceinline__ void feed_next(const HeadsArgs& a, const Lane& l, Fee
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// A head's codes and scale into the cache: x of its lane, the clamped maximum
-// over its lanes.  EXACT: see quantise.
-template <int G, bool EXACT>
+// A head's codes and scale into the cache: x and the largest magnitude of the
+// lane.
+template <int G>
 __device__ __forceinline__ void store_codes(const HeadsArgs& a, float2 x[8], float m, bool store,
                                             bool first_lane, uint8_t* codes, float* scales,
                                             int64_t code_at, int64_t scale_at, int da, int db) {
@@ -306,7 +305,7 @@ __device__ __forceinline__ void store_codes(const HeadsArgs& a, float2 x[8], flo
     const bool clamped = m > a.scale_ub;
     m = fmaxf(fminf(m, a.scale_ub), 1e-12f);
     uint2 qa, qb;
-    const float scale = quantise<EXACT>(x, m, clamped, qa, qb);
+    const float scale = quantise(x, m, clamped, qa, qb);
     if (store && RRF_IN_BOUNDS(code_at >= 0 && code_at + a.dim <= a.code_end && scale_at >= 0 &&
                                    scale_at < a.scale_end,
                                a.err)) {
@@ -361,10 +360,8 @@ __device__ __forceinline__ void work_chunks(const HeadsArgs& a, const Lane& l, c
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
             }
-            store_codes<G, KIND == kValue>(a, x, m, left > 0, l.g == 0,
-                                           KIND == kKey ? a.k_codes : a.v_codes,
-                                           KIND == kKey ? a.k_scales : a.v_scales, code_at,
-                                           scale_at, da, db);
+            store_codes<G>(a, x, m, left > 0, l.g == 0, KIND == kKey ? a.k_codes : a.v_codes,
+                           KIND == kKey ? a.k_scales : a.v_scales, code_at, scale_at, da, db);
             code_at += kHeads * a.code_head;
             scale_at += kHeads * a.scale_head;
         }
@@ -515,8 +512,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) write_kernel(const HeadsA
         bf16x8_to_f32x2(rb, x + 4);
         feed();
         if (place.x < 0) continue;  // uniform in the warp
-        store_codes<G, true>(a, x, max_bf16x16(ra, rb), mine, l.g == 0, codes, scales,
-                             place.x + code_head, place.y + scale_head, da, db);
+        store_codes<G>(a, x, max_bf16x16(ra, rb), mine, l.g == 0, codes, scales,
+                       place.x + code_head, place.y + scale_head, da, db);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }

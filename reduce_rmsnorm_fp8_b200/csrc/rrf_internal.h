@@ -109,6 +109,10 @@ struct ArLaunch {
 // and up to 4 vectors per thread fit the register budget of 512 threads).
 constexpr int kArMaxThreads = 512;
 
+// GemmArgs.act of the calls without an epilogue, which keep plan_scaled_mm's
+// kernels; the others take plan_scaled_mm_act's.
+constexpr int kPlainProduct = -1;
+
 // The FP8 GEMM (rrf_gemm.cu); the operands themselves reach the kernel as
 // tensor maps.
 struct GemmArgs {
@@ -119,7 +123,7 @@ struct GemmArgs {
     int M, N, K;
     unsigned int* err;
     int starve;            // test hook: the epilogue's extra wait runs out
-    int act;               // RRF_ACT_*
+    int act;               // RRF_ACT_*, or kPlainProduct
     const uint16_t* residual;  // bf16 [M, N] or null; may be out
 };
 
@@ -251,6 +255,7 @@ struct GemmPlan {
     int64_t ctas;
 };
 GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count);
+GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_count);
 cudaError_t launch_scaled_mm(const GemmArgs& g, const void* a, const void* b, int sm_count,
                              cudaStream_t stream);
 // The MX GEMM: sfa / sfb are the scale codes in the blocked order; g.a_scale

@@ -17,6 +17,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
+SMS = 148  # B200
 ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
 
 
@@ -94,32 +95,41 @@ def check(p, got, act, residual, label=""):
     assert worst <= 1.0, f"{label} {act}: {worst:.3f} of the bound"
 
 
-# every kernel of the planner, per row / column scales and MX
-FP8 = [(1, 256, 128, "swap"), (9, 528, 640, "swap"), (24, 336, 1536, "swap"), (3, 320, 1152, "swap"),
-       (32, 7168, 512, "swap"), (5, 256, 144, "tile"), (64, 1024, 1024, "tile"),
-       (37, 256, 256, "tile"), (130, 400, 144, "tile"), (200, 272, 384, "tile"),
-       (1000, 2576, 272, "tile"), (2000, 2576, 1040, "pair"), (4096, 4112, 16, "pair")]
-MX = [(1, 256, 128, "swap"), (16, 208, 1408, "swap"), (29, 128, 1664, "swap"),
-      (60, 1040, 384, "tile"), (200, 272, 384, "tile"), (1000, 2576, 256, "tile"),
-      (2000, 2576, 640, "pair")]
+# every kernel of the planner (kernel, A rows, columns), per row / column scales
+# and MX
+FP8 = [(1, 256, 128, "swap", 8, 64), (9, 528, 640, "swap", 16, 64),
+       (24, 336, 1536, "swap", 32, 64), (3, 320, 1152, "swap", 8, 64),
+       (32, 7168, 512, "swap", 32, 64), (5, 256, 144, "tile", 64, 64),
+       (64, 1024, 1024, "tile", 64, 64), (37, 272, 256, "tile", 64, 64),
+       (50, 16400, 1024, "tile", 64, 128), (130, 400, 144, "tile", 128, 64),
+       (200, 272, 384, "tile", 128, 64), (250, 7184, 272, "tile", 128, 128),
+       (800, 2320, 2048, "tile", 128, 128), (500, 7168, 2048, "pair", 256, 256),
+       (2000, 2576, 8208, "pair", 256, 256), (4096, 8192, 1040, "pair", 256, 256)]
+MX = [(1, 256, 128, "swap", 8, 64), (16, 208, 1408, "swap", 16, 64),
+      (29, 128, 1664, "swap", 32, 64), (60, 1040, 384, "tile", 64, 64),
+      (33, 16400, 640, "tile", 64, 128), (200, 272, 384, "tile", 128, 64),
+      (800, 2320, 1024, "tile", 128, 128), (500, 7168, 2048, "pair", 256, 256),
+      (2000, 8208, 1152, "pair", 256, 256)]
 
 
 @pytest.mark.parametrize("act", ACTS)
-@pytest.mark.parametrize("m,n,k,kernel,mx", [(*s, False) for s in FP8] + [(*s, True) for s in MX])
-def test_matches_float64(rrf, m, n, k, kernel, mx, act):
-    sms = torch.cuda.get_device_properties(0).multi_processor_count
-    assert rrf.rrf_plan_scaled_mm(m, n, k, sms, mx=mx)["kernel"] == kernel
+@pytest.mark.parametrize("m,n,k,kernel,rows,columns,mx",
+                         [(*s, False) for s in FP8] + [(*s, True) for s in MX])
+def test_matches_float64(rrf, m, n, k, kernel, rows, columns, mx, act):
+    plan = rrf.rrf_plan_scaled_mm_act(m, n, k, SMS, mx=mx)
+    assert (plan["kernel"], plan["a_rows"], plan["tile_n"]) == (kernel, rows, columns), plan
     for bias, residual in ((True, True), (False, True), (True, False), (False, False)):
         p = problem(rrf, m + n + k, m, n, k, mx, bias, residual, spread=2.0)
         check(p, call(rrf, p, act), act, p["residual"], f"bias {bias} residual {residual}")
 
 
 @pytest.mark.parametrize("m,n,k,mx", [(8, 16384, 1024, False), (32, 16384, 512, True),
-                                      (64, 16384, 512, False), (100, 16384, 256, True),
-                                      (4096, 4096, 512, False), (4096, 4096, 512, True)])
+                                      (64, 10240, 512, False), (64, 37888, 1024, False), (50, 37888, 1024, True),
+                                      (100, 10240, 256, True), (4096, 4096, 512, False),
+                                      (4096, 4096, 512, True), (4096, 4096, 2048, False),
+                                      (4096, 4096, 2048, True)])
 def test_several_tiles_of_a_block(rrf, m, n, k, mx):
-    sms = torch.cuda.get_device_properties(0).multi_processor_count
-    plan = rrf.rrf_plan_scaled_mm(m, n, k, sms, mx=mx)
+    plan = rrf.rrf_plan_scaled_mm_act(m, n, k, SMS, mx=mx)
     assert plan["tiles"] > plan["ctas"] // (2 if plan["kernel"] == "pair" else 1), plan
     p = problem(rrf, m, m, n, k, mx)
     check(p, call(rrf, p, "silu"), "silu", p["residual"])
