@@ -1576,11 +1576,9 @@ extern "C" rrf_status rrf_kv_cache_read_fp8(const rrf_kv_cache* cache,
     a.k_out = static_cast<uint16_t*>(k_out);
     a.v_out = static_cast<uint16_t*>(v_out);
     a.rows = (int)rows;
-    int sm_count = 0;
-    if ((st = current_sm_count(&sm_count)) != RRF_OK) return st;
     if ((st = device_error_word(&a.err)) != RRF_OK) return st;
     cudaError_t e;
-    if (!take_injected_failure(&e)) e = launch_cache_read(a, sm_count, (cudaStream_t)stream);
+    if (!take_injected_failure(&e)) e = launch_cache_read(a, (cudaStream_t)stream);
     return e == cudaSuccess ? RRF_OK : cuda_fail(e);
 }
 

@@ -16,7 +16,7 @@
 // A persistent CTA per SM walks 128 x BN tiles of out (BN 128 or 64).
 // Warp roles (the same in every kernel; the swapped kernel's MX form adds a
 // seventh warp that rearranges the scale codes of each stage, and tiles of 128
-// columns and more have eight epilogue warps):
+// columns have eight epilogue warps, those of 256 sixteen):
 //   warp 0   one thread issues the TMA loads of the A (128 x 128 bytes) and
 //            B (BN x 128 bytes) k-tiles into a ring of shared-memory stages
 //            (128-byte swizzle, the layout the MMA descriptors name);
@@ -166,6 +166,36 @@ __device__ __forceinline__ void tmem_load_32(uint32_t taddr, float v[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// NA consecutive fp32 accumulator columns of this thread's lane (NA = 8, 16
+// or 32).
+template <int NA>
+__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, float v[NA]) {
+    uint32_t r[NA];
+    if constexpr (NA == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < NA; ++i) v[i] = __uint_as_float(r[i]);
+    } else if constexpr (NA == 16) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+            "%10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < NA; ++i) v[i] = __uint_as_float(r[i]);
+    } else {
+        static_assert(NA == 32, "8, 16 or 32 columns");
+        tmem_load_32(taddr, v);
+    }
+}
+
 // Shared-memory matrix descriptor of a K-major tile stored as rows of 128
 // bytes in 128-byte-swizzled 1024-byte atoms (8 rows each), the layout a
 // TMA load with CU_TENSOR_MAP_SWIZZLE_128B writes: start address >> 4,
@@ -284,9 +314,11 @@ __device__ __forceinline__ void activate_all(int act, float2 y[PAIRS]) {
 // B200, 4096 x 4096 x 1024 with silu and residual: 88.9 us with each lane
 // reading and writing its own row 64 bytes at a time and its column scales one
 // by one; 35.1 us through shared memory with the warp's own coalesced loads
-// and stores; 32.5 us with TMA.  (The products alone take 15 us there: at so
-// short a K the epilogue's shared-memory traffic, 5 passes over 64 KB a tile,
-// meets the operands' in the same banks.)
+// and stores; 32.5 us with TMA and eight warps a CTA; 29.2 us with sixteen.
+// (The products alone take 15 us there: at so short a K the epilogue's
+// shared-memory traffic, 5 passes over 64 KB a tile, meets the operands' in the
+// same banks.  At 8192^3 the power limit bounds both: 1.4 GHz, 452 us without
+// and 484 with gelu and residual.)
 constexpr int kChunk = 64;               // columns of a chunk
 constexpr int kBoxBytes = 32 * kChunk * 2;
 
@@ -378,38 +410,36 @@ struct EpiWarp {
         columns[lane] = make_float4(scale.x, scale.y, bias.x, bias.y);
         __syncwarp();
         if (more) load_columns(n_next);
+        // 16 columns at a time, in a loop: the block's many warps hide one
+        // another's latency, and the code stays short
+#pragma unroll 1
+        for (int h = 0; h < kChunk / 16; ++h) {
+            float v[16];
+            tmem_load_cols<16>(taddr + 16 * h, v);
+            if (h == kChunk / 16 - 1) after_read();
+            float2 y[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[32];
-            tmem_load_32(taddr + 32 * h, v);
-            if (h == 1) after_read();
-            float2 y[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 s = columns[16 * h + i];
+            for (int i = 0; i < 8; ++i) {
+                const float4 s = columns[8 * h + i];
                 y[i] = make_float2(v[2 * i], v[2 * i + 1]);
                 if constexpr (SCALED)
                     y[i] = __fmul2_rn(__fmul2_rn(y[i], both(sa)), make_float2(s.x, s.y));
                 y[i] = __fadd2_rn(y[i], make_float2(s.z, s.w));
             }
-            activate_all<16>(g.act, y);
+            activate_all<8>(g.act, y);
             uint4* row = box + lane * 8;
+            uint4& lo = row[(2 * h) ^ (lane & 7)];
+            uint4& hi = row[(2 * h + 1) ^ (lane & 7)];
             if (g.residual != nullptr) {
-                uint4 res[4];
+                float2 r[8];
+                bf16x8_to_f32x2(lo, r);
+                bf16x8_to_f32x2(hi, r + 4);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) res[q] = row[(4 * h + q) ^ (lane & 7)];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float2 r[4];
-                    bf16x8_to_f32x2(res[q], r);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[4 * q + i] = __fadd2_rn(y[4 * q + i], r[i]);
-                }
+                for (int i = 0; i < 8; ++i) y[i] = __fadd2_rn(y[i], r[i]);
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                row[(4 * h + q) ^ (lane & 7)] = f32x2_to_bf16x8(y + 4 * q);
-            if (h == 0 && BOXES > 1) {
+            lo = f32x2_to_bf16x8(y);
+            hi = f32x2_to_bf16x8(y + 4);
+            if (h == 1 && BOXES > 1) {
                 // the other box's store began a chunk ago
                 boxes_free();
                 if (more) load_box(row_next, n_next);
@@ -821,36 +851,6 @@ __device__ __forceinline__ uint16_t ld_residual(const uint16_t* p) {
     return v;
 }
 
-// NA consecutive fp32 accumulator columns of this thread's lane (NA = 8, 16
-// or 32).
-template <int NA>
-__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, float v[NA]) {
-    uint32_t r[NA];
-    if constexpr (NA == 8) {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                       "=r"(r[6]), "=r"(r[7])
-                     : "r"(taddr));
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < NA; ++i) v[i] = __uint_as_float(r[i]);
-    } else if constexpr (NA == 16) {
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-            "%10, %11, %12, %13, %14, %15}, [%16];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-            : "r"(taddr));
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < NA; ++i) v[i] = __uint_as_float(r[i]);
-    } else {
-        static_assert(NA == 32, "8, 16 or 32 columns");
-        tmem_load_32(taddr, v);
-    }
-}
-
 // sfx, sfw: the MX form's scale codes of the call's rows and of the weight
 // (the blocked order); null in the per-token form.
 template <int NA, int Z, bool MX>
@@ -1251,11 +1251,11 @@ __device__ __forceinline__ void grouped_tile(int t, int tiles_m, int tiles_n, in
     tn = r / rows;
 }
 
-// Eight epilogue warps in each CTA of a pair: two for each 32 rows, on every
-// other 64 columns.
-constexpr int kPairEpiWarps = 8;
+// Sixteen epilogue warps in each CTA of a pair: one for each 32 rows and each
+// 64 columns.
+constexpr int kPairEpiWarps = 16;
 constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
-constexpr int kPairBoxes = 2;   // of each epilogue warp (1 and a fifth stage: 25% slower at K = 1024)
+constexpr int kPairBoxes = 1;
 constexpr int kPairStages = 4;
 
 struct PairTile {
@@ -1412,8 +1412,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const float sa = row0 + lane < g.M ? g.a_scale[row0 + lane] : 0.0f;
             const uint32_t base = tmem + (uint32_t)(buf * BN + group * kChunk) +
                                   ((uint32_t)(quarter * 32) << 16);
-            if (!epi.chunk(base, sa, row0, n0, true, row0, n0 + 128, [] {})) break;
-            if (!epi.chunk(base + 128, sa, row0, n0 + 128, more, row_next, n_next, [&]() {
+            if (!epi.chunk(base, sa, row0, n0, more, row_next, n_next, [&]() {
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(leader_acc_empty[buf]);
@@ -1864,45 +1863,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     } else {
         // ---- epilogue (each CTA): its 128 accumulator rows.  The 32 columns
-        // that the two buffers share (the last of buffer 0, the first of
-        // buffer 1) lie in the chunk that one of the two groups reads first.
+        // that the two buffers share are the last of buffer 0 (group 3 reads
+        // them) and the first of buffer 1 (group 0).
         const int quarter = warp & 3, group = (warp - 2) >> 2;
         T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, warp - 2, lane);
         const uint32_t leader_acc_empty[2] = {peer_smem(&acc_empty[0], 0),
                                               peer_smem(&acc_empty[1], 0)};
         const uint32_t leader_ovl_free = peer_smem(ovl_free, 0);
-        // buffer 0: columns 192.. and 64.. (group 1), 128.. and 0.. (group 0);
-        // buffer 1: 64.. and 192.., 0.. and 128..
         int tm, tn;
         grouped_tile(pair, tiles_m, tiles_n, tm, tn);
-        int row0 = tm * 256 + (int)rank * 128 + quarter * 32, n0 = tn * 256;
-        epi.ahead(row0, n0 + group * kChunk + 128);
+        int row0 = tm * 256 + (int)rank * 128 + quarter * 32, n0 = tn * 256 + group * kChunk;
+        epi.ahead(row0, n0);
         int j = 0;
         for (int t = pair; t < tiles; t += npairs, ++j) {
             const int buf = j & 1;
             const bool more = t + npairs < tiles;
             if (more) grouped_tile(t + npairs, tiles_m, tiles_n, tm, tn);
-            const int row_next = tm * 256 + (int)rank * 128 + quarter * 32, n_next = tn * 256;
+            const int row_next = tm * 256 + (int)rank * 128 + quarter * 32;
+            const int n_next = tn * 256 + group * kChunk;
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
             if (!__all_sync(0xFFFFFFFFu, have)) break;
             tc_fence_after_sync();
-            const uint32_t base =
-                tmem + (buf ? T::kBuf1 : 0u) + ((uint32_t)(quarter * 32) << 16);
-            const int c0 = group * kChunk + (buf ? 0 : 128), c1 = group * kChunk + (buf ? 128 : 0);
-            if (!epi.chunk(base + (uint32_t)c0, 1.0f, row0, n0 + c0, true, row0, n0 + c1, [&]() {
-                    if (group != (buf ? 0 : 1)) return;
+            const uint32_t base = tmem + (buf ? T::kBuf1 : 0u) + (uint32_t)(group * kChunk) +
+                                  ((uint32_t)(quarter * 32) << 16);
+            if (!epi.chunk(base, 1.0f, row0, n0, more, row_next, n_next, [&]() {
                     tc_fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(leader_ovl_free);
+                    if (lane == 0) {
+                        if (group == (buf ? 0 : 3)) mbar_arrive_cluster(leader_ovl_free);
+                        mbar_arrive_cluster(leader_acc_empty[buf]);
+                    }
                 }))
-                break;
-            // the next tile's first chunk is that of the other buffer
-            if (!epi.chunk(base + (uint32_t)c1, 1.0f, row0, n0 + c1, more, row_next,
-                           n_next + group * kChunk + (buf ? 128 : 0), [&]() {
-                               tc_fence_before_sync();
-                               __syncwarp();
-                               if (lane == 0) mbar_arrive_cluster(leader_acc_empty[buf]);
-                           }))
                 break;
             row0 = row_next;
             n0 = n_next;

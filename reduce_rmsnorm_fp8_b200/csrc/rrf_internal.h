@@ -186,6 +186,10 @@ struct CacheReadArgs {
     uint16_t* v_out;
     int rows;
     unsigned int* err;
+    // set by the launcher: ceil(2^32 / (dim / 16)), and whether both outputs
+    // are aligned to 32 bytes
+    uint32_t head_magic;
+    bool whole;
 };
 
 struct FusedLaunch {
@@ -234,7 +238,7 @@ cudaError_t launch_post(const PostArgs& a, int sm_count, bool pdl, cudaStream_t 
 // norm: q and k are normalised, rotated and written; else k and v go to the
 // cache as they are.
 cudaError_t launch_heads(const HeadsArgs& a, bool norm, int sm_count, cudaStream_t stream);
-cudaError_t launch_cache_read(const CacheReadArgs& a, int sm_count, cudaStream_t stream);
+cudaError_t launch_cache_read(CacheReadArgs a, cudaStream_t stream);
 
 cudaError_t launch_allreduce(const ArArgs& a, const ArLaunch& l, cudaStream_t stream);
 // The GEMM kernel a shape takes (pure host arithmetic; the launchers follow

@@ -347,6 +347,19 @@ def test_read_of_fewer_rows_and_wide_tables(rrf):
     check_read(cache, table, starts + 4, out)
 
 
+@pytest.mark.parametrize("which", [0, 1])
+def test_read_to_outputs_aligned_to_16_bytes(rrf, which):
+    cache, table, starts, out = read_problem(3, [20, 5], 9, 16, 3, 80)
+    n = out[which].numel()
+    odd = torch.full((n + 16,), 3.0 + which, dtype=torch.bfloat16, device="cuda")
+    at = 8 if odd.data_ptr() % 32 == 0 else 16
+    out[which] = odd[at:at + n].view(out[which].shape)
+    assert out[which].data_ptr() % 32 == 16
+    rrf.rrf_kv_cache_read_fp8(*cache, table, starts, *out)
+    check_read(cache, table, starts, out)
+    assert bool((odd[:at] == 3 + which).all()) and bool((odd[at + n:] == 3 + which).all())
+
+
 @pytest.mark.parametrize("bad", [-1, 9, 2 ** 31 - 1, -2 ** 31])
 def test_pages_outside_the_cache_are_left_out(rrf, bad):
     cache, table, starts, out = read_problem(2, [20, 5], 9, 16, 2, 64)
