@@ -84,7 +84,7 @@ def build_binding(force: bool = False) -> str:
               sysconfig.get_paths()["include"]):
         cmd += ["-isystem", d]
     cmd += [TORCH_SRC, "-o", tmp, "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
-            "-ltorch_cpu", "-ltorch_python"]
+            "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on rrf_torch.cpp:\n{r.stdout}\n{r.stderr}")

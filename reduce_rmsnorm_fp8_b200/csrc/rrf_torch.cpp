@@ -9,7 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -93,7 +93,9 @@ int device_of(const at::Tensor& t, const char* name) {
 }
 
 at::Tensor fresh(at::IntArrayRef shape, int index) {
-    return at::empty(shape, at::TensorOptions().dtype(at::kBFloat16).device(at::kCUDA, index));
+    return at::detail::empty_cuda(shape, at::kBFloat16,
+                                  at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)),
+                                  c10::nullopt);
 }
 
 // call(stream) on the device and its current stream.

@@ -123,8 +123,35 @@ def test_matches_float64(rrf, m, n, k, kernel, rows, columns, mx, act):
         check(p, call(rrf, p, act), act, p["residual"], f"bias {bias} residual {residual}")
 
 
+@pytest.mark.parametrize("m", [1, 5, 33, 64, 70, 200])
+@pytest.mark.parametrize("n,k,mx", [(16, 128, False), (32, 144, False), (48, 16, False),
+                                    (16, 128, True), (80, 256, True)])
+def test_narrow_products(rrf, m, n, k, mx):
+    """Fewer columns than a tile, a chunk or a box."""
+    p = problem(rrf, m + n, m, n, k, mx)
+    guard = torch.full((m * n + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = guard[64:64 + m * n].view(m, n)
+    check(p, call(rrf, p, "gelu", out=out), "gelu", p["residual"])
+    assert bool((guard[:64] == 7).all()) and bool((guard[64 + m * n:] == 7).all())
+
+
+@pytest.mark.parametrize("m", [3, 40, 100, 600])
+def test_scales_and_bias_of_any_alignment(rrf, m):
+    """The row and column scales need 4 bytes, the bias 2."""
+    p = problem(rrf, m, m, 2576, 256)
+    want = call(rrf, p, "silu")
+    for name in ("sa", "sb", "bias"):
+        x = p[name]
+        wide = torch.zeros(x.numel() + 1, dtype=x.dtype, device="cuda")
+        wide[1:] = x
+        p[name] = wide[1:]
+        assert p[name].data_ptr() % 16 == x.element_size()
+    assert torch.equal(call(rrf, p, "silu"), want)
+
+
 @pytest.mark.parametrize("m,n,k,mx", [(8, 16384, 1024, False), (32, 16384, 512, True),
-                                      (64, 10240, 512, False), (64, 37888, 1024, False), (50, 37888, 1024, True),
+                                      (64, 10240, 512, False), (64, 37888, 1024, False),
+                                      (50, 37888, 1024, True),
                                       (100, 10240, 256, True), (4096, 4096, 512, False),
                                       (4096, 4096, 512, True), (4096, 4096, 2048, False),
                                       (4096, 4096, 2048, True)])
