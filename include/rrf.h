@@ -567,10 +567,14 @@ rrf_status rrf_check_scaled_mm_mx_act_args(const void* a, const void* sa, const 
 #define RRF_GEMM_KERNEL_SWAP 3 /* operands swapped, 64 weight rows of each of two
                                   k-tiles on the MMA's M side, the call's rows padded
                                   to a_rows (per-token and MX, at most 32 rows)       */
+#define RRF_GEMM_KERNEL_SPLIT 4 /* rrf_scaled_mm_*_act: a cluster of ctas / tiles CTAs
+                                  for each a_rows x 64 tile, K split among them       */
 
 /* rrf_plan_scaled_mm_act -- as rrf_plan_scaled_mm, below, for
  * rrf_scaled_mm_fp8_act (mx == 0) and rrf_scaled_mm_mxfp8_act (mx != 0): the
- * same kernels, chosen by the measured time of a round of tiles. */
+ * same kernels and RRF_GEMM_KERNEL_SPLIT, chosen by the measured time of a
+ * round of tiles.  (So the two calls' sums over K may round differently from
+ * rrf_scaled_mm_fp8's and rrf_scaled_mm_mxfp8's.) */
 rrf_status rrf_plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, int mx, int sm_count,
                                   int* kernel, int* a_rows, int* tile_n, int* k_tiles_per_stage,
                                   int64_t* tiles, int64_t* ctas);
@@ -805,7 +809,7 @@ int rrf_last_cuda_error(void);
 void rrf_debug_fail_next_launch(int cuda_error);
 
 /* Test hook for the GEMMs' bounded waits: the next rrf_scaled_mm_fp8 or
- * rrf_scaled_mm_mxfp8 call on this host thread that launches (a call
+ * rrf_scaled_mm_mxfp8 call (or its _act form) on this host thread that launches (a call
  * rejected on the host, or with M == 0, leaves the hook set) runs, but its
  * epilogue, after each accumulator it drains, also waits for that
  * accumulator's next completion, which cannot come before the epilogue

@@ -48,7 +48,7 @@ _EXPORTS = (
     "mx_blocked", "mx_blocked_bytes", "rrf_scaled_mm_mxfp8", "rrf_check_scaled_mm_mx_args",
     "RRF_AR_STATIC_MAX_WORLD", "rrf_allreduce_rmsnorm_fp8_static_ptr",
     "rrf_plan_scaled_mm", "rrf_plan_scaled_mm_act", "RRF_GEMM_KERNEL_PAIR", "RRF_GEMM_KERNEL_TILE",
-    "RRF_GEMM_KERNEL_SWAP", "RRF_FLAG_NO_PREFETCH", "RRF_FLAG_PREFETCH", "rrf_plan_fused_ex",
+    "RRF_GEMM_KERNEL_SWAP", "RRF_GEMM_KERNEL_SPLIT", "RRF_FLAG_NO_PREFETCH", "RRF_FLAG_PREFETCH", "rrf_plan_fused_ex",
     "RRF_DEVICE_ERROR_BOUNDS", "RRF_DEVICE_ERROR_INDEX", "RRF_MAX_HEAD_DIM", "RRF_ACT_NONE",
     "RRF_ACT_RELU", "RRF_ACT_GELU", "RRF_ACT_GELU_TANH", "RRF_ACT_SILU",
 )

@@ -37,6 +37,7 @@ RRF_MAX_HEAD_DIM = 512
 RRF_GEMM_KERNEL_PAIR = 1
 RRF_GEMM_KERNEL_TILE = 2
 RRF_GEMM_KERNEL_SWAP = 3
+RRF_GEMM_KERNEL_SPLIT = 4
 RRF_ACT_NONE = 0
 RRF_ACT_RELU = 1
 RRF_ACT_GELU = 2
@@ -561,7 +562,7 @@ def _plan_scaled_mm(plan, M, N, K, sm_count, mx):
     longs = [_i64() for _ in range(2)]
     _raise_on(plan(M, N, K, int(bool(mx)), sm_count, *[ctypes.byref(o) for o in ints + longs]))
     names = {RRF_GEMM_KERNEL_PAIR: "pair", RRF_GEMM_KERNEL_TILE: "tile",
-             RRF_GEMM_KERNEL_SWAP: "swap"}
+             RRF_GEMM_KERNEL_SWAP: "swap", RRF_GEMM_KERNEL_SPLIT: "split"}
     return {"kernel": names.get(ints[0].value), "a_rows": ints[1].value,
             "tile_n": ints[2].value, "k_tiles_per_stage": ints[3].value,
             "tiles": longs[0].value, "ctas": longs[1].value}

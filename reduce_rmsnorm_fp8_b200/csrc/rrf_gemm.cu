@@ -12,7 +12,10 @@
 //            (BN 128 or 64), Z k-tiles per TMA box for short products;
 //   scaled_mm_swap_pairk_kernel  at most 32 rows against a weight, the
 //            operands swapped (the weight's rows on the MMA's M side, two
-//            k-tiles of them per instruction); per-token and MX forms.
+//            k-tiles of them per instruction); per-token and MX forms;
+//   scaled_mm_split_kernel  products of few tiles, K split among the CTAs of
+//            a cluster; per-token and MX forms (only the calls with an
+//            epilogue, see plan_scaled_mm_act).
 // A persistent CTA per SM walks 128 x BN tiles of out (BN 128 or 64).
 // Warp roles (the same in every kernel; the swapped kernel's MX form adds a
 // seventh warp that rearranges the scale codes of each stage, and tiles of 128
@@ -851,6 +854,15 @@ __device__ __forceinline__ uint16_t ld_residual(const uint16_t* p) {
     return v;
 }
 
+__device__ __forceinline__ uint4 ld_residual(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // sfx, sfw: the MX form's scale codes of the call's rows and of the weight
 // (the blocked order); null in the per-token form.
 template <int NA, int Z, bool MX>
@@ -1655,6 +1667,232 @@ __global__ void __launch_bounds__(MxTile<BN, AROWS, Z>::kThreadsPerCta, 1)
     }
 }
 
+// ------------------------------------------------- split over K (clusters) --
+// A product of few tiles (a narrow weight against few rows) leaves most SMs
+// idle while each tile's CTA streams its whole K.  Here a cluster of S CTAs
+// (2, 4 or 8) shares a tile of AROWS x 64: each takes a part of K, then sends
+// every row of its partial sums to the CTA of the cluster that finishes the
+// row (row r: CTA r / (AROWS / S)), which adds the S parts in the order of
+// their ranks and runs the epilogue on its rows.  The parts travel through
+// distributed shared memory: no workspace, and the same bits every time.
+// B200: 64 x 1024 x 7168 in 7.2 us by 4 CTAs to a tile (15.6 us by one).
+template <int AROWS, bool MX>
+struct SplitTile {
+    static constexpr int kBN = 64;
+    static constexpr int Z = AROWS == kBM ? 2 : 4;  // k-tiles per stage
+    static constexpr int kABytes = AROWS * kBK;
+    static constexpr int kBBytes = kBN * kBK;
+    static constexpr int kBOffset = Z * kABytes;
+    static constexpr int kSfBytes = 512;
+    static constexpr int kSfaOffset = Z * (kABytes + kBBytes);
+    static constexpr int kSfbOffset = kSfaOffset + Z * kSfBytes;
+    static constexpr int kStageBytes = MX ? kSfbOffset + Z * kSfBytes : kSfaOffset;
+    static constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
+    static constexpr int kStages = AROWS == 32 ? 4 : 3;
+    // the parts: S x (AROWS / S) rows of 64 sums, 68 apart (16-byte stores of
+    // neighbouring rows then meet in no bank)
+    static constexpr int kPitch = kBN + 4;
+    static constexpr int kPartsOffset = kStages * kStageStride;
+    static constexpr int kBarrierOffset = kPartsOffset + AROWS * kPitch * 4;
+    static constexpr int kBarriers = 2 * kStages + 2;
+    static constexpr int kTmemCols = MX ? 128 : 64;
+    static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
+    static_assert(kSmemBytes <= 227 * 1024, "stages exceed the shared memory of a CTA");
+    static_assert((Z - 1) * kABytes + kBM * kBK <= Z * (kABytes + kBBytes),
+                  "the MMA's 128 rows of A must stay inside the stage");
+};
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                 :: "r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+template <int AROWS, bool MX>
+__global__ void __launch_bounds__(kThreads, 1)
+    scaled_mm_split_kernel(const __grid_constant__ CUtensorMap tma_a,
+                           const __grid_constant__ CUtensorMap tma_b, const GemmArgs g,
+                           const uint8_t* sfa, const uint8_t* sfb, int split) {
+    using T = SplitTile<AROWS, MX>;
+    constexpr int S = T::kStages, Z = T::Z, BN = T::kBN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    float* parts = reinterpret_cast<float*>(smem + T::kPartsOffset);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::kBarrierOffset);
+    uint64_t* empty = full + S;
+    uint64_t* acc_full = empty + S;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int tile = (int)blockIdx.x / split;
+    const int tiles_n = (g.N + BN - 1) / BN;
+    const int m0 = (tile / tiles_n) * kBM, n0 = (tile % tiles_n) * BN;
+    const int ktiles = g.K / kBK;  // K is a multiple of 128
+    const int kgroups = (ktiles + Z - 1) / Z;
+    const int k_lo = rank * kgroups / split, k_hi = (rank + 1) * kgroups / split;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        fence_mbar_init_cluster();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, T::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    // every CTA of the cluster has started before any writes into another
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    wait_for_previous_grid();
+    allow_next_grid();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int kg = k_lo; kg < k_hi; ++kg, ++it) {
+                const int s = it % S;
+                if (!wait_phase(&empty[s], ((it / S) & 1) ^ 1, g.err)) break;
+                uint8_t* dst = smem + s * T::kStageStride;
+                const int nk = ktiles - kg * Z < Z ? ktiles - kg * Z : Z;
+                const uint32_t sf_bytes = MX ? (uint32_t)(nk * T::kSfBytes) : 0u;
+                mbar_arrive_expect_tx(&full[s], Z * (T::kABytes + T::kBBytes) + 2 * sf_bytes);
+                tma_load_3d(dst, &tma_a, &full[s], 0, m0, kg * Z);
+                tma_load_3d(dst + T::kBOffset, &tma_b, &full[s], 0, n0, kg * Z);
+                if constexpr (MX) {
+                    bulk_load(dst + T::kSfaOffset,
+                              sfa + ((int64_t)(m0 / 128) * ktiles + kg * Z) * T::kSfBytes,
+                              sf_bytes, &full[s]);
+                    bulk_load(dst + T::kSfbOffset,
+                              sfb + ((int64_t)(n0 / 128) * ktiles + kg * Z) * T::kSfBytes,
+                              sf_bytes, &full[s]);
+                }
+            }
+            // the loads still in flight land before the CTA may exit
+            for (int i = it > S ? it - S : 0; i < it; ++i)
+                wait_phase(&full[i % S], (i / S) & 1, g.err);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t tmem_sfa = tmem + BN;
+            const uint32_t tmem_sfb = tmem_sfa + 4;
+            // the odd 64-column half of a scale atom: 2 columns further on
+            const uint32_t sfb_cols = tmem_sfb + (uint32_t)((n0 / BN) & 1) * 2u;
+            int it = 0;
+            for (int kg = k_lo; kg < k_hi; ++kg, ++it) {
+                const int s = it % S;
+                if (!wait_phase(&full[s], (it / S) & 1, g.err)) break;
+                tc_fence_after_sync();
+                const uint8_t* stage = smem + s * T::kStageStride;
+                const int nk = ktiles - kg * Z < Z ? ktiles - kg * Z : Z;
+                for (int kj = 0; kj < nk; ++kj) {
+                    if constexpr (MX) {
+                        tmem_copy_32x128b_x4(tmem_sfa,
+                                             sf_atom_desc(stage + T::kSfaOffset + kj * T::kSfBytes));
+                        tmem_copy_32x128b_x4(tmem_sfb,
+                                             sf_atom_desc(stage + T::kSfbOffset + kj * T::kSfBytes));
+                    }
+                    const uint64_t ad = kmajor_sw128_desc(stage + kj * T::kABytes);
+                    const uint64_t bd = kmajor_sw128_desc(stage + T::kBOffset + kj * T::kBBytes);
+#pragma unroll
+                    for (int k = 0; k < kBK / kMmaK; ++k) {
+                        const uint64_t step = (uint64_t)(k * kMmaK) >> 4;
+                        if constexpr (MX)
+                            mma_mx(tmem, ad + step, bd + step, mx_idesc(BN, (uint32_t)k),
+                                   (it | kj | k) != 0, tmem_sfa, sfb_cols);
+                        else
+                            mma_f8(tmem, ad + step, bd + step, f8_idesc(BN), (it | kj | k) != 0);
+                    }
+                }
+                mma_commit(&empty[s]);
+            }
+            mma_commit(acc_full);
+        }
+        __syncwarp();
+    } else {
+        // ---- each lane's row of sums to the CTA that finishes it
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane, own = AROWS / split;
+        bool have = epilogue_wait(acc_full, 0, g);
+        have = __all_sync(0xFFFFFFFFu, have);
+        tc_fence_after_sync();
+        if (quarter * 32 < AROWS && m0 + quarter * 32 < g.M && have) {
+            const uint32_t to = peer_smem(
+                parts + (rank * own + row % own) * T::kPitch, (uint32_t)(row / own));
+#pragma unroll
+            for (int c = 0; c < BN; c += 16) {
+                float v[16];
+                tmem_load_cols<16>(tmem + (uint32_t)c + ((uint32_t)(quarter * 32) << 16), v);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    st_cluster_v4(to + (uint32_t)(c + i) * 4,
+                                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+            }
+        }
+        tc_fence_before_sync();
+    }
+    // every part is where it is added, and this CTA's tensor memory is read
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    if (warp == 1) {
+        // (an accumulator whose wait ran out may still be written)
+        wait_phase(acc_full, 0, g.err);
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, T::kTmemCols);
+    }
+    if (warp < 2) return;
+
+    // ---- the epilogue of this CTA's rows, 8 columns to a thread
+    const int own = AROWS / split;
+    for (int i = (int)threadIdx.x - 64; i < own * (BN / 8); i += kThreads - 64) {
+        const int r = i / (BN / 8), c = i % (BN / 8) * 8;
+        const int row = m0 + rank * own + r, n = n0 + c;
+        if (row >= g.M || n >= g.N || !RRF_IN_BOUNDS(row >= 0 && n >= 0, g.err)) continue;
+        const int64_t at = (int64_t)row * g.N + n;
+        uint4 res = make_uint4(0, 0, 0, 0);
+        if (g.residual != nullptr) res = ld_residual(reinterpret_cast<const uint4*>(g.residual + at));
+        float2 y[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = both(0.0f);
+        for (int p = 0; p < split; ++p) {
+            const float4* part =
+                reinterpret_cast<const float4*>(parts + (p * own + r) * T::kPitch + c);
+            const float4 u = part[0], w = part[1];
+            y[0] = __fadd2_rn(y[0], make_float2(u.x, u.y));
+            y[1] = __fadd2_rn(y[1], make_float2(u.z, u.w));
+            y[2] = __fadd2_rn(y[2], make_float2(w.x, w.y));
+            y[3] = __fadd2_rn(y[3], make_float2(w.z, w.w));
+        }
+        const float sa = MX ? 1.0f : g.a_scale[row];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int col = n + 2 * q;
+            if constexpr (!MX)
+                y[q] = __fmul2_rn(__fmul2_rn(y[q], both(sa)),
+                                  make_float2(g.b_scale[col], g.b_scale[col + 1]));
+            if (g.bias != nullptr)
+                y[q] = __fadd2_rn(y[q], make_float2(__uint_as_float((uint32_t)g.bias[col] << 16),
+                                                    __uint_as_float((uint32_t)g.bias[col + 1] << 16)));
+        }
+        activate_all<4>(g.act, y);
+        if (g.residual != nullptr) {
+            float2 add[4];
+            bf16x8_to_f32x2(res, add);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] = __fadd2_rn(y[q], add[q]);
+        }
+        *reinterpret_cast<uint4*>(g.out + at) = f32x2_to_bf16x8(y);
+    }
+}
+
 // --------------------------------------------- MX GEMM on SM pairs (2 CTAs) --
 // The block-scaled MMA with cta_group::2 on 256 x 256 tiles, as the per-token
 // pair kernel: each CTA loads 128 rows of A and 128 rows of B per k-tile.
@@ -2134,6 +2372,43 @@ cudaError_t launch_mx(const GemmArgs& g, const void* a, const void* b, const uin
                              g, sfa, sfb);
 }
 
+// Clusters of `split` CTAs, one for each AROWS x 64 tile.
+template <int AROWS, bool MX>
+cudaError_t launch_split(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
+                         const uint8_t* sfb, int64_t tiles, int split, cudaStream_t stream) {
+    using T = SplitTile<AROWS, MX>;
+    CUtensorMap ma, mb;
+    if (!make_map3(&ma, a, g.M, g.K, AROWS, T::Z) || !make_map3(&mb, b, g.N, g.K, T::kBN, T::Z))
+        return cudaErrorInvalidValue;
+    constexpr auto kernel = scaled_mm_split_kernel<AROWS, MX>;
+    const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = T::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, g, sfa, sfb, split);
+}
+
+template <bool MX>
+cudaError_t launch_split_rows(const GemmPlan& p, const GemmArgs& g, const void* a, const void* b,
+                              const uint8_t* sfa, const uint8_t* sfb, cudaStream_t stream) {
+    const int split = (int)(p.ctas / p.tiles);
+    if (p.a_rows == 32) return launch_split<32, MX>(g, a, b, sfa, sfb, p.tiles, split, stream);
+    if (p.a_rows == 64) return launch_split<64, MX>(g, a, b, sfa, sfb, p.tiles, split, stream);
+    return launch_split<kBM, MX>(g, a, b, sfa, sfb, p.tiles, split, stream);
+}
+
 cudaError_t launch_mx_pair(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
                            const uint8_t* sfb, int sm_count, cudaStream_t stream) {
     using T = MxPairTile;
@@ -2209,26 +2484,37 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
 
 // The products with an epilogue.  A persistent CTA (or pair) takes its tiles
 // in rounds, and a round's time is near a fixed part e plus the k-tiles times
-// c, whatever M and N.  Measured on B200 (us; N = 1024 .. 16384, M = 48 ..
-// 4096, K = 1024 and 4096, silu and residual):
-//   64 columns, 64-row A stages      e 0.3  c 0.24    (K % 128 != 0: c 0.35)
-//   64 columns, 128 rows             e 0.7  c 0.254   (K % 128 != 0: c 0.35)
-//   128 columns, 64-row A stages     e 1.5  c 0.26
-//   128 columns, 128 rows            e 2.0  c 0.2875
-//   256 x 256 on SM pairs            e 5.0  c 0.29
+// c, whatever M and N.  Measured on B200 (us above the 3.7 of an empty call; N
+// = 256 .. 16384, M = 1 .. 4096, K = 1024 .. 7168, silu and residual):
+//   swapped, at most 8 / 16 / 32 rows  e 0 / 0 / 0.3  c 0.085 / 0.113 / 0.135
+//                       (MX: c 0.15 / 0.15 / 0.18)
+//   64 columns, 64-row A stages        e 0.3  c 0.24    (K % 128 != 0: c 0.35)
+//   64 columns, 128 rows               e 0.7  c 0.254   (K % 128 != 0: c 0.35)
+//   128 columns, 64-row A stages       e 1.5  c 0.26
+//   128 columns, 128 rows              e 2.0  c 0.2875
+//   256 x 256 on SM pairs              e 5.0  c 0.29
+//   K split, 32 / 64 / 128 rows        e 0 / 0.3 / 1.7  c 0.21 / 0.225 / 0.25
+//                       of the k-tiles of one CTA, rounded up to its stages
 // (the operands that a CTA loads per k-tile count, hardly its products: 64
 // columns cost nearly as much as 128).  The kernel of the least rounds * (e +
-// k-tiles * c) is taken; at most 32 rows stay with the swapped kernel.
-// Against plan_scaled_mm's choice: 512 x 7168 x 4096 22.9 (pairs) for 27.1 us,
-// 256 x 7168 x 4096 16.7 (128 columns) for 21.6, 64 x 16384 x 7168 25.8 (128
-// columns) for 31.3, MX 1999 x 2576 x 1024 15.6 (128 columns) for 18.1.
+// k-tiles * c) is taken.  K is split among as many CTAs as are resident at
+// once (of clusters of 2, 4 and 8: 74, 32 and 15).  Against plan_scaled_mm's
+// choice: 64 x 1024 x 7168 7.2 (split in 4) for 15.6 us, 1 x 1024 x 7168 6.7
+// for 8.5, 128 x 2048 x 7168 9.6 for 18.3, 512 x 7168 x 4096 22.9 (pairs) for
+// 27.1, 256 x 7168 x 4096 16.7 (128 columns) for 21.6, 64 x 16384 x 7168 25.8
+// (128 columns) for 31.3, MX 1999 x 2576 x 1024 15.6 (128 columns) for 18.1.
 GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) {
     GemmPlan best = plan_scaled_mm(M, N, K, mx, sm_count);
-    if (best.kernel == kGemmSwap) return best;
     const bool atoms = K % kBK == 0;  // several k-tiles per box
-    const double ktiles = (double)((K + kBK - 1) / kBK);
+    const int64_t ktiles = (K + kBK - 1) / kBK;
     double least = 0.0;
-    auto offer = [&](int kernel, int arows, int bn, int z, double e, double c) {
+    auto offer = [&](const GemmPlan& p, double cost) {
+        if (least == 0.0 || cost < least) {
+            least = cost;
+            best = p;
+        }
+    };
+    auto offer_tile = [&](int kernel, int arows, int bn, int z, double e, double c) {
         GemmPlan p;
         p.kernel = kernel;
         p.a_rows = arows;
@@ -2238,21 +2524,43 @@ GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_cou
         const int64_t units = kernel == kGemmPair ? sm_count / 2 : sm_count;
         p.tiles = ((M + rows - 1) / rows) * ((N + bn - 1) / bn);
         p.ctas = (p.tiles < units ? p.tiles : units) * (kernel == kGemmPair ? 2 : 1);
-        const double cost = (double)((p.tiles + units - 1) / units) * (e + ktiles * c);
-        if (least == 0.0 || cost < least) {
-            least = cost;
-            best = p;
-        }
+        offer(p, (double)((p.tiles + units - 1) / units) * (e + (double)ktiles * c));
     };
-    if (M <= 64) {
-        offer(kGemmTile, 64, 64, atoms ? 4 : 1, 0.3, atoms ? 0.24 : 0.35);
-        if (atoms) offer(kGemmTile, 64, 128, 2, 1.5, 0.26);
+    if (best.kernel == kGemmSwap) {
+        const double c = M <= 8    ? (mx ? 0.15 : 0.085)
+                         : M <= 16 ? (mx ? 0.15 : 0.113)
+                                   : (mx ? 0.18 : 0.135);
+        const int64_t rounds = (best.tiles + sm_count - 1) / sm_count;
+        offer(best, (double)rounds * ((M > 16 ? 0.3 : 0.0) + (double)ktiles * c));
+    } else {
+        if (M <= 64) {
+            offer_tile(kGemmTile, 64, 64, atoms ? 4 : 1, 0.3, atoms ? 0.24 : 0.35);
+            if (atoms) offer_tile(kGemmTile, 64, 128, 2, 1.5, 0.26);
+        } else {
+            offer_tile(kGemmTile, kBM, 64, atoms ? 2 : 1, 0.7, atoms ? 0.254 : 0.35);
+        }
+        if (M > 64 || !atoms) offer_tile(kGemmTile, kBM, 128, 1, 2.0, 0.2875);
+        if (M > 128) offer_tile(kGemmPair, 256, 256, 1, 5.0, 0.29);
     }
-    if (M > 64 || !atoms) {
-        if (M > 64) offer(kGemmTile, kBM, 64, atoms ? 2 : 1, 0.7, atoms ? 0.254 : 0.35);
-        offer(kGemmTile, kBM, 128, 1, 2.0, 0.2875);
+    if (atoms) {
+        GemmPlan p;
+        p.kernel = kGemmSplit;
+        p.a_rows = M <= 32 ? 32 : M <= 64 ? 64 : kBM;
+        p.tile_n = 64;
+        p.k_tiles_per_stage = M <= 64 ? 4 : 2;
+        p.tiles = ((M + kBM - 1) / kBM) * ((N + 63) / 64);
+        const int64_t groups = (ktiles + p.k_tiles_per_stage - 1) / p.k_tiles_per_stage;
+        const double e = M <= 32 ? 0.0 : M <= 64 ? 0.3 : 1.7;
+        const double c = M <= 32 ? 0.21 : M <= 64 ? 0.225 : 0.25;
+        const int64_t resident[3] = {sm_count / 2, (int64_t)32 * sm_count / 148,
+                                     (int64_t)15 * sm_count / 148};
+        for (int i = 0; i < 3; ++i) {
+            const int64_t split = 2 << i;
+            if (p.tiles > resident[i] || groups < split) continue;  // (a CTA has a group at least)
+            p.ctas = p.tiles * split;
+            offer(p, e + (double)((groups + split - 1) / split * p.k_tiles_per_stage) * c);
+        }
     }
-    if (M > 128) offer(kGemmPair, 256, 256, 1, 5.0, 0.29);
     return best;
 }
 
@@ -2261,6 +2569,7 @@ cudaError_t launch_scaled_mm_mx(const GemmArgs& g, const void* a, const void* b,
                                 cudaStream_t stream) {
     const GemmPlan p = g.act == kPlainProduct ? plan_scaled_mm(g.M, g.N, g.K, true, sm_count)
                                  : plan_scaled_mm_act(g.M, g.N, g.K, true, sm_count);
+    if (p.kernel == kGemmSplit) return launch_split_rows<true>(p, g, a, b, sfa, sfb, stream);
     if (p.kernel == kGemmPair) return launch_mx_pair(g, a, b, sfa, sfb, sm_count, stream);
     if (p.kernel == kGemmSwap) {
         if (p.a_rows == 8) return launch_swap_pairk<8, 4, true>(g, a, b, sm_count, stream, sfa, sfb);
@@ -2279,6 +2588,8 @@ cudaError_t launch_scaled_mm(const GemmArgs& g, const void* a, const void* b, in
                              cudaStream_t stream) {
     const GemmPlan p = g.act == kPlainProduct ? plan_scaled_mm(g.M, g.N, g.K, false, sm_count)
                                  : plan_scaled_mm_act(g.M, g.N, g.K, false, sm_count);
+    if (p.kernel == kGemmSplit)
+        return launch_split_rows<false>(p, g, a, b, nullptr, nullptr, stream);
     if (p.kernel == kGemmPair) return launch_pair(g, a, b, sm_count, stream);
     if (p.kernel == kGemmSwap) {
         if (p.a_rows == 8) return launch_swap_pairk<8, 8>(g, a, b, sm_count, stream);

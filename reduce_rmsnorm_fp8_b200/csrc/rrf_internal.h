@@ -250,6 +250,7 @@ cudaError_t launch_allreduce(const ArArgs& a, const ArLaunch& l, cudaStream_t st
 constexpr int kGemmPair = RRF_GEMM_KERNEL_PAIR;
 constexpr int kGemmTile = RRF_GEMM_KERNEL_TILE;
 constexpr int kGemmSwap = RRF_GEMM_KERNEL_SWAP;
+constexpr int kGemmSplit = RRF_GEMM_KERNEL_SPLIT;
 struct GemmPlan {
     int kernel;
     int a_rows;

@@ -53,38 +53,55 @@ def test_cpu_tensors_and_unknown_activations_are_refused(rrf):
         rrf.rrf_scaled_mm_fp8_act(a, s, a, s)
 
 
-def test_plan(rrf):
-    """The plan follows the measured time of a round, for every shape: no other
-    kernel's rounds would take less, and the CTAs cover the tiles."""
-    cost = {("tile", 64, 64): (0.3, 0.24), ("tile", 128, 64): (0.7, 0.254),
-            ("tile", 64, 128): (1.5, 0.26), ("tile", 128, 128): (2.0, 0.2875),
-            ("pair", 256, 256): (5.0, 0.29)}
-    seen = set()
-    for m in (1, 8, 31, 33, 64, 65, 129, 300, 1000, 4096):
-        for n in (16, 256, 1024, 7168, 16384):
-            for k in (128, 1024, 7168):
+@pytest.mark.parametrize("m,n,k,mx,want", [
+    (1, 7168, 7168, False, ("swap", 8, 64, 8, 112, 112)),
+    (64, 16384, 7168, False, ("tile", 64, 128, 2, 128, 128)),
+    (64, 7168, 7168, False, ("tile", 64, 64, 4, 112, 112)),
+    (128, 7168, 4096, False, ("tile", 128, 64, 2, 112, 112)),
+    (256, 7168, 4096, False, ("tile", 128, 128, 1, 112, 112)),
+    (512, 7168, 4096, False, ("pair", 256, 256, 1, 56, 112)),
+    (8192, 8192, 8192, False, ("pair", 256, 256, 1, 1024, 148)),
+    (1, 1024, 7168, False, ("split", 32, 64, 4, 16, 64)),
+    (64, 960, 7168, False, ("split", 64, 64, 4, 15, 120)),
+    (128, 2048, 7168, False, ("split", 128, 64, 2, 32, 128)),
+    (1999, 2576, 1024, True, ("tile", 128, 128, 1, 336, 148)),
+    (64, 1024, 7168, True, ("split", 64, 64, 4, 16, 64)),
+    (40, 4096, 1040, False, ("tile", 64, 64, 1, 64, 64))])  # K % 128 != 0
+def test_plan(rrf, m, n, k, mx, want):
+    p = rrf.rrf_plan_scaled_mm_act(m, n, k, 148, mx=mx)
+    assert (p["kernel"], p["a_rows"], p["tile_n"], p["k_tiles_per_stage"], p["tiles"],
+            p["ctas"]) == want
+
+
+@pytest.mark.parametrize("sms", [148, 132, 40])
+def test_plan_invariants(rrf, sms):
+    for m in (1, 8, 9, 31, 33, 64, 65, 129, 300, 1000, 4096):
+        for n in (16, 256, 1024, 4096, 7168, 16384):
+            for k in (16, 128, 512, 1040, 2048, 7168):
                 for mx in (False, True):
-                    p = rrf.rrf_plan_scaled_mm_act(m, n, k, 148, mx=mx)
-                    if m <= 32:
-                        assert p == rrf.rrf_plan_scaled_mm(m, n, k, 148, mx=mx)
+                    if mx and k % 128:
                         continue
-                    key = (p["kernel"], p["a_rows"], p["tile_n"])
-                    seen.add(key)
-                    taken = {}
-                    for (kernel, rows, columns), (e, c) in cost.items():
-                        fits = m <= 64 if rows == 64 else m > 64 if rows == 128 else m > 128
-                        if not fits:
-                            continue
-                        units, high = (74, 256) if kernel == "pair" else (148, 128)
-                        tiles = -(-m // high) * -(-n // columns)
-                        taken[kernel, rows, columns] = -(-tiles // units) * (e + k / 128 * c)
-                        if (kernel, rows, columns) == key:
-                            assert p["tiles"] == tiles
-                            assert p["ctas"] == min(tiles, units) * (2 if kernel == "pair" else 1)
-                    assert taken[key] <= min(taken.values()) + 1e-9
-    assert seen == set(cost)
-    # K % 128 != 0: one k-tile per box
-    for m in (40, 100):
-        assert rrf.rrf_plan_scaled_mm_act(m, 4096, 1040, 148)["k_tiles_per_stage"] == 1
+                    p = rrf.rrf_plan_scaled_mm_act(m, n, k, sms, mx=mx)
+                    kernel, rows, columns = p["kernel"], p["a_rows"], p["tile_n"]
+                    high = 256 if kernel == "pair" else 128
+                    if kernel != "swap":
+                        assert p["tiles"] == -(-m // high) * -(-n // columns)
+                    if kernel == "split":
+                        split, left = divmod(p["ctas"], p["tiles"])
+                        assert split in (2, 4, 8) and left == 0 and p["ctas"] <= sms
+                        # every CTA has a part of K
+                        assert k % 128 == 0 and -(-k // 128 // p["k_tiles_per_stage"]) >= split
+                        assert rows >= min(m, 128)
+                    else:
+                        assert p["ctas"] == min(p["tiles"], sms // 2) * 2 if kernel == "pair" \
+                            else p["ctas"] == min(p["tiles"], sms)
+                    if kernel == "tile":
+                        assert (rows == 64) == (m <= 64 and not (columns == 128 and k % 128))
+
+
+def test_plan_refusals(rrf):
     with pytest.raises(rrf.RrfError):
         rrf.rrf_plan_scaled_mm_act(8, 256, 1040, 148, mx=True)
+    with pytest.raises(rrf.RrfError):
+        rrf.rrf_plan_scaled_mm_act(8, 256, 1024, 1)
+    assert rrf.rrf_plan_scaled_mm_act(0, 256, 1024, 148)["kernel"] is None

@@ -95,21 +95,31 @@ def check(p, got, act, residual, label=""):
     assert worst <= 1.0, f"{label} {act}: {worst:.3f} of the bound"
 
 
-# every kernel of the planner (kernel, A rows, columns), per row / column scales
-# and MX
+# every kernel of the planner (kernel, A rows, columns; a split kernel's CTAs to
+# a tile), per row / column scales and MX
 FP8 = [(1, 256, 128, "swap", 8, 64), (9, 528, 640, "swap", 16, 64),
-       (24, 336, 1536, "swap", 32, 64), (3, 320, 1152, "swap", 8, 64),
+       (24, 336, 384, "swap", 32, 64), (3, 320, 1152, "swap", 8, 64),
        (32, 7168, 512, "swap", 32, 64), (5, 256, 144, "tile", 64, 64),
-       (64, 1024, 1024, "tile", 64, 64), (37, 272, 256, "tile", 64, 64),
+       (64, 5120, 1024, "tile", 64, 64), (37, 272, 256, "tile", 64, 64),
        (50, 16400, 1024, "tile", 64, 128), (130, 400, 144, "tile", 128, 64),
        (200, 272, 384, "tile", 128, 64), (250, 7184, 272, "tile", 128, 128),
        (800, 2320, 2048, "tile", 128, 128), (500, 7168, 2048, "pair", 256, 256),
-       (2000, 2576, 8208, "pair", 256, 256), (4096, 8192, 1040, "pair", 256, 256)]
-MX = [(1, 256, 128, "swap", 8, 64), (16, 208, 1408, "swap", 16, 64),
-      (29, 128, 1664, "swap", 32, 64), (60, 1040, 384, "tile", 64, 64),
+       (2000, 2576, 8208, "pair", 256, 256), (4096, 8192, 1040, "pair", 256, 256),
+       (24, 336, 1536, "split", 32, 2), (31, 2064, 7168, "split", 32, 2),
+       (1, 2000, 4224, "split", 32, 4), (8, 912, 4224, "split", 32, 8),
+       (64, 4624, 1664, "split", 64, 2), (40, 1040, 3200, "split", 64, 4),
+       (33, 272, 7168, "split", 64, 8), (100, 4624, 2048, "split", 128, 2),
+       (250, 784, 3456, "split", 128, 4), (129, 336, 4352, "split", 128, 8)]
+MX = [(1, 256, 128, "swap", 8, 64), (16, 208, 512, "swap", 16, 64),
+      (29, 7168, 1664, "swap", 32, 64), (60, 1040, 384, "tile", 64, 64),
       (33, 16400, 640, "tile", 64, 128), (200, 272, 384, "tile", 128, 64),
       (800, 2320, 1024, "tile", 128, 128), (500, 7168, 2048, "pair", 256, 256),
-      (2000, 8208, 1152, "pair", 256, 256)]
+      (2000, 8208, 1152, "pair", 256, 256),
+      (20, 4624, 1536, "split", 32, 2), (2, 2000, 2176, "split", 32, 4),
+      (32, 912, 4224, "split", 32, 8), (64, 4624, 1664, "split", 64, 2),
+      (40, 1104, 3200, "split", 64, 4), (33, 336, 7168, "split", 64, 8),
+      (100, 4624, 2048, "split", 128, 2), (250, 784, 3456, "split", 128, 4),
+      (129, 336, 4352, "split", 128, 8)]
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -117,7 +127,8 @@ MX = [(1, 256, 128, "swap", 8, 64), (16, 208, 1408, "swap", 16, 64),
                          [(*s, False) for s in FP8] + [(*s, True) for s in MX])
 def test_matches_float64(rrf, m, n, k, kernel, rows, columns, mx, act):
     plan = rrf.rrf_plan_scaled_mm_act(m, n, k, SMS, mx=mx)
-    assert (plan["kernel"], plan["a_rows"], plan["tile_n"]) == (kernel, rows, columns), plan
+    last = plan["ctas"] // plan["tiles"] if kernel == "split" else plan["tile_n"]
+    assert (plan["kernel"], plan["a_rows"], last) == (kernel, rows, columns), plan
     for bias, residual in ((True, True), (False, True), (True, False), (False, False)):
         p = problem(rrf, m + n + k, m, n, k, mx, bias, residual, spread=2.0)
         check(p, call(rrf, p, act), act, p["residual"], f"bias {bias} residual {residual}")
@@ -162,10 +173,11 @@ def test_several_tiles_of_a_block(rrf, m, n, k, mx):
     check(p, call(rrf, p, "silu"), "silu", p["residual"])
 
 
-@pytest.mark.parametrize("m,mx", [(1, False), (20, True), (60, False), (300, False), (3000, True),
-                                  (3000, False)])
-def test_residual_in_place(rrf, m, mx):
-    p = problem(rrf, 7, m, 2064, 256, mx)
+@pytest.mark.parametrize("m,k,mx", [(1, 256, False), (20, 256, True), (60, 256, False),
+                                    (300, 256, False), (3000, 256, True), (3000, 256, False),
+                                    (7, 4096, False), (60, 4096, True), (100, 4096, False)])
+def test_residual_in_place(rrf, m, k, mx):
+    p = problem(rrf, 7, m, 2064, k, mx)
     keep = p["residual"].clone()
     out = call(rrf, p, "gelu", out=p["residual"])
     assert out.data_ptr() == p["residual"].data_ptr()
@@ -271,3 +283,20 @@ def test_refusals_of_tensors(rrf):
         buf = torch.empty(9 * 64, dtype=torch.bfloat16, device="cuda")
         f(*args, residual=buf[:512].view(8, 64), out=buf[64:].view(8, 64))
     assert e.value.status == rrf.Status.ERR_ALIAS
+
+
+@pytest.mark.parametrize("m,n,k,mx", [(4, 1024, 4096, False), (60, 1024, 4096, True),
+                                      (200, 7168, 1024, False), (600, 7168, 2048, False)])
+def test_wait_timeout_is_reported(rrf, m, n, k, mx):
+    """The test hook makes a bounded wait of the epilogue run out: the call ends,
+    reports it, and the next call is right.  Two calls of a split product give
+    the same bits."""
+    p = problem(rrf, 5, m, n, k, mx)
+    torch.cuda.synchronize()
+    rrf.rrf_debug_starve_next_gemm()
+    call(rrf, p, "silu")
+    torch.cuda.synchronize()
+    assert rrf.rrf_device_error(clear=True) & rrf.RRF_DEVICE_ERROR_GEMM_TIMEOUT
+    out = call(rrf, p, "silu")
+    check(p, out, "silu", p["residual"])
+    assert torch.equal(out, call(rrf, p, "silu"))
