@@ -38,10 +38,15 @@ constexpr int kStages = 4;        // (6 stages: 51.2 us, and slower at small hea
 constexpr int kStageVecs = 2 * 32 * kWarpsPerBlock;  // 16-byte vectors of a block's stage
 // 5 blocks an SM, 96 registers: 51.4 us; 4 (no spills): 51.8; 6: 56.0.
 constexpr int kBlocksPerSm = 5;
-// Warps an SM should get before a warp is given more than one chunk of a
-// token (or, writing alone, more than one token).  512 tokens x 72 heads: 12
-// warps 5.7 us, 24 6.8 us, 40 8.7 us; no difference at 8192.
-constexpr int kWarpsWanted = 12;
+// The work of a warp, in chunks of a token (or, writing alone, in tokens of a
+// chunk).  Blocks run in rounds of as many as are resident, and a warp's time
+// is near its chunks plus a set-up of kSetUp chunks, so the launch takes the
+// split of the least rounds * (chunks + kSetUp).  B200, 72 heads of 128:
+// 4096 tokens 27.7 us with 9 chunks a warp (3 rounds) against 30.1 with all 18
+// (2 rounds), 1536 tokens 12.7 with 6 against 14.1, 8192 tokens 51.4 with 18
+// against 51.7 with 9.
+constexpr double kSetUp = 2.5;
+constexpr int kWriteBlocksPerSm = 7;
 
 __device__ __forceinline__ void load4(const float* p, float2 v[2]) {
     const float4 f = *reinterpret_cast<const float4*>(p);
@@ -409,6 +414,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, kBlocksPerSm) heads_kerne
     Lane l;
     l.token = opaque((int)blockIdx.x) * kWarpsPerBlock + (threadIdx.x >> 5);
     if (l.token >= a.tokens) return;
+    // the token's slot and position, on their way while the lane sets itself up
+    const int64_t slot = a.slots != nullptr ? a.slots[l.token] : -1;
+    const int64_t pos = a.rot > 0 ? a.positions[l.token] : 0;
     place_lane<G>(a, l);
     const int lo = blockIdx.y * a.per;
     const int hi = lo + a.per < a.chunks ? lo + a.per : a.chunks;
@@ -424,16 +432,10 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, kBlocksPerSm) heads_kerne
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) feed_next<G>(a, l, feed, next, hi);
 
-    l.cached = false;
-    l.code_at = l.scale_at = 0;
-    if (a.slots != nullptr) l.cached = place_of(a, a.slots[l.token], l.code_at, l.scale_at);
-    bool valid = true;
-    if (a.rot > 0) {
-        const int64_t pos = a.positions[l.token];
-        valid = pos >= 0 && pos < a.max_positions;
-        if (!valid) atomicOr(a.err, RRF_DEVICE_ERROR_INDEX);
-        l.turn = a.cos_sin + (valid ? pos : 0) * a.rot;
-    }
+    const bool valid = a.rot == 0 || (pos >= 0 && pos < a.max_positions);
+    if (!valid) atomicOr(a.err, RRF_DEVICE_ERROR_INDEX);
+    l.turn = a.cos_sin + (valid ? pos : 0) * a.rot;
+    l.cached = place_of(a, slot, l.code_at, l.scale_at);
     if (valid) {
         const int k0 = lo > a.key_chunk ? lo : a.key_chunk;
         const int v0 = lo > a.value_chunk ? lo : a.value_chunk;
@@ -540,19 +542,29 @@ cudaError_t launch_lanes(HeadsArgs a, bool norm, int sm_count, cudaStream_t stre
     a.key_chunk = norm ? (a.q.heads + kHeads - 1) / kHeads : 0;
     a.value_chunk = a.key_chunk + kv_chunks;
     a.chunks = a.value_chunk + (a.slots != nullptr ? kv_chunks : 0);
-    // chunks of a warp: as many as leave kWarpsWanted warps per SM
-    const int64_t each = (int64_t)a.tokens * a.chunks / ((int64_t)sm_count * kWarpsWanted);
-    if (norm) {
-        a.per = each < 1 ? 1 : each > a.chunks ? a.chunks : (int)each;
-        const int parts = (a.chunks + a.per - 1) / a.per;
-        a.per = (a.chunks + parts - 1) / parts;  // the same for each
-        return launch(heads_kernel<G>, a, ((int64_t)a.tokens + kWarpsPerBlock - 1) / kWarpsPerBlock,
-                      parts, stream);
+    // blocks for `per` units of work to a warp, and the best `per` up to `most`
+    const auto blocks_of = [&](int per) {
+        const int64_t warps = norm ? a.tokens : ((int64_t)a.tokens + per - 1) / per;
+        const int64_t y = norm ? (a.chunks + per - 1) / per : a.chunks;
+        return (warps + kWarpsPerBlock - 1) / kWarpsPerBlock * y;
+    };
+    const int64_t resident = (int64_t)sm_count * (norm ? kBlocksPerSm : kWriteBlocksPerSm);
+    const int most = norm ? a.chunks : 32;  // (a write warp's lanes hold its places)
+    double least = 0.0;
+    for (int units = most, parts = 1; units >= 1; ++parts) {
+        const int64_t rounds = (blocks_of(units) + resident - 1) / resident;
+        const double cost = (double)rounds * (units + kSetUp);
+        if (least == 0.0 || cost < least) {
+            least = cost;
+            a.per = units;
+        }
+        if (units == 1) break;
+        while ((most + parts - 1) / parts >= units) ++parts;  // the next smaller split
+        units = (most + parts - 1) / parts;
     }
-    a.per = each < 1 ? 1 : each > 32 ? 32 : (int)each;
-    const int64_t warps = ((int64_t)a.tokens + a.per - 1) / a.per;
-    return launch(write_kernel<G>, a, (warps + kWarpsPerBlock - 1) / kWarpsPerBlock, a.chunks,
-                  stream);
+    const int64_t y = norm ? (a.chunks + a.per - 1) / a.per : a.chunks;
+    const int64_t x = blocks_of(a.per) / y;
+    return norm ? launch(heads_kernel<G>, a, x, y, stream) : launch(write_kernel<G>, a, x, y, stream);
 }
 
 }  // namespace
