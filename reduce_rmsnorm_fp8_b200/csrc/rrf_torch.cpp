@@ -6,6 +6,7 @@
 // at a dozen tensors and passing thirty arguments from Python took 9 to 17 us
 // a call.  The module calls the C functions of the library that the package
 // has loaded (bind(), called once), so there is one librrf.so in a process.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
@@ -120,8 +121,8 @@ PyObject* guarded(Py_ssize_t nargs, Py_ssize_t want, Body body) {
         return body();
     } catch (const Refused& e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, e.what());
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // torch's own (out of memory, a CUDA error) as torch raises them
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

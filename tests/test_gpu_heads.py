@@ -504,6 +504,52 @@ def test_current_stream_is_used(rrf):
     assert all(torch.equal(a, b) for a, b in zip(want, (s["q_out"], *s["out"])))
 
 
+def test_two_streams_at_once(rrf):
+    """Calls that overlap on the GPU share nothing."""
+    states = [step_problem(rrf, 20 + n, tokens=512, hidden=1024) for n in range(2)]
+    streams = [torch.cuda.Stream() for _ in states]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, stream in zip(states, streams):
+            with torch.cuda.stream(stream):
+                step(rrf, s)
+    torch.cuda.synchronize()
+    for s in states:
+        check_step(s)
+
+
+def test_refusals_of_tensors(rrf):
+    """Each refusal names its tensor, and nothing is written."""
+    q, k, v, qg, kg, table, pos = problem(2, 6, 2, 1, 64, 64)
+    cache = new_cache(gen(1), 4, 16, 1, 64)
+    before = clone_cache(cache)
+    slots = torch.arange(6, device="cuda")
+    args = dict(q=q, k=k, v=v, q_gamma=qg, k_gamma=kg, eps=1e-6, weight_offset=0.0, cos_sin=table,
+                positions=pos, slots=slots, k_cache=cache[0], k_scales=cache[1],
+                v_cache=cache[2], v_scales=cache[3])
+    wide = torch.zeros((6, 2, 128), dtype=torch.bfloat16, device="cuda")
+    for name, bad in [("q", q.float()), ("q", q[:, 0]), ("k", k[:5]), ("k", k[..., :32]),
+                      ("v", v.transpose(1, 2).contiguous().transpose(1, 2)[:, :, :1]),
+                      ("q", wide[..., ::2]), ("q_gamma", qg[:32]), ("k_gamma", kg.float()),
+                      ("cos_sin", table.double()), ("cos_sin", table[:, ::2]),
+                      ("positions", pos.int()), ("positions", pos[:5]), ("positions", None),
+                      ("slots", slots.int()), ("slots", slots[:5]), ("slots", slots.cpu()),
+                      ("k_cache", cache[0].view(torch.uint8)), ("k_cache", cache[0][:, :8]),
+                      ("v_cache", cache[2].transpose(1, 3)), ("k_scales", cache[1].double()),
+                      ("v_scales", cache[3][:3]), ("q", None), ("k_cache", 3)]:
+        with pytest.raises(ValueError, match="cache|scales" if name[1:] in ("_cache", "_scales")
+                           else name):
+            rrf.rrf_qk_norm_rope_kv_cache_fp8(**{**args, name: bad})
+    with pytest.raises(rrf.RrfError) as e:
+        rrf.rrf_qk_norm_rope_kv_cache_fp8(**{**args, "eps": -1.0})
+    assert e.value.status == rrf.Status.ERR_VALUE
+    with pytest.raises(rrf.RrfError) as e:  # heads on one another
+        rrf.rrf_qk_norm_rope_kv_cache_fp8(**args, q_out=q[:, :1].expand(6, 2, 64))
+    assert e.value.status == rrf.Status.ERR_ALIAS
+    for a, b in zip(clone_cache(cache), before):
+        assert torch.equal(a, b)
+
+
 def test_empty_calls(rrf):
     q, k, v, qg, kg, table, pos = problem(1, 1, 2, 1, 64, 64)
     cache = new_cache(gen(1), 2, 16, 1, 64)
