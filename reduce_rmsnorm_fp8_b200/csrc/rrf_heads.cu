@@ -46,7 +46,11 @@ constexpr int kBlocksPerSm = 5;
 // (2 rounds), 1536 tokens 12.7 with 6 against 14.1, 8192 tokens 51.4 with 18
 // against 51.7 with 9.
 constexpr double kSetUp = 2.5;
+// Writing alone: 7 blocks an SM.  Compiled for 5 it takes 68 registers, of which
+// 7 blocks still fit; compiled for 7 (62 registers) the loads are further from
+// their use and 8192 tokens of 8 + 8 heads of 128 take 11.2 us against 10.3.
 constexpr int kWriteBlocksPerSm = 7;
+constexpr int kWriteBlocksCompiled = 5;
 
 __device__ __forceinline__ void load4(const float* p, float2 v[2]) {
     const float4 f = *reinterpret_cast<const float4*>(p);
@@ -77,32 +81,27 @@ __device__ __forceinline__ float fast_reciprocal(float v) {
     return r;
 }
 
-// The codes of x[16] under m, their clamped maximum, and the row's scale.
+// The codes of x[16], a row of largest magnitude `most`, and the row's scale.
 // For values that are bf16, x / scale = 448 x / m is often exactly a midpoint
 // of the e4m3 grid, and a product with a rounded reciprocal would land on
 // either side of it.  So the quotient of n = 448 x (exact then) is corrected
 // once by its exact remainder (Markstein's final step, y + (n - y m) / m),
 // which makes a representable quotient exact and any other one correct to
-// about half an ulp.
-// Rows above 1e30 are scaled by 2^-64 first, so that 448 x stays finite, and
-// values beyond a clamped maximum are cut to it (they saturate).
-__device__ __forceinline__ float quantise(float2 x[8], float m, bool clamped, uint2& qa,
+// about half an ulp.  Rows above 1e30 are scaled by 2^-64 first, so that n
+// stays finite.  Values beyond a bound (scale_ub) saturate; only where they are
+// 1e30 times the bound, and y might not be finite, is it left uncorrected.
+// (Cutting x to the bound instead cost every row 20 of 185 instructions.)
+__device__ __forceinline__ float quantise(const float2 x[8], float most, float scale_ub, uint2& qa,
                                           uint2& qb) {
-    if (clamped) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // (a NaN stays one)
-            x[i].x = x[i].x > m ? m : x[i].x < -m ? -m : x[i].x;
-            x[i].y = x[i].y > m ? m : x[i].y < -m ? -m : x[i].y;
-        }
-    }
-    const float down = m > 1e30f ? 5.421010862427522e-20f : 1.0f;  // 2^-64
+    const float m = fmaxf(fminf(most, scale_ub), 1e-12f);
+    const float down = most > 1e30f ? 5.421010862427522e-20f : 1.0f;  // 2^-64
     const float d = m * down, f = 448.0f * down, inv = fast_reciprocal(d);
     const float2 k2 = make_float2(f * inv, f * inv);
     float2 y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(x[i], k2);
     // (an infinite scale: finite values are 0, infinities NaN)
-    if (d < __int_as_float(0x7F800000)) {
+    if (most <= m * 1e30f && d < __int_as_float(0x7F800000)) {
         const float2 minus_d = make_float2(-d, -d), f2 = make_float2(f, f);
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
@@ -118,14 +117,16 @@ __device__ __forceinline__ float quantise(float2 x[8], float m, bool clamped, ui
                : s;
 }
 
-// The largest magnitude of 16 bf16 (max.bf16x2, like fmaxf, passes over a NaN).
+// The largest magnitude of 16 bf16 (like fmaxf, it passes over a NaN).
 __device__ __forceinline__ float max_bf16x16(const uint4 u, const uint4 v) {
     const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
+    uint32_t m = w[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
-    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    for (int i = 1; i < 8; ++i)  // (magnitudes; the sign is of no use)
+        asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+    // (0 where all are NaN)
+    return fmaxf(0.0f, fmaxf(fabsf(__uint_as_float(m << 16)),
+                             fabsf(__uint_as_float(m & 0xFFFF0000u))));
 }
 
 // n / d for n >= 0, d > 0, in 32 bits where they do.
@@ -300,23 +301,29 @@ __device__ __forceinline__ void feed_next(const HeadsArgs& a, const Lane& l, Fee
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
+// (the bounds-checking build) Eight codes at `codes` and `second` further on,
+// and a scale, lie in the keys' or the values' arrays.
+[[maybe_unused]] __device__ __forceinline__ bool in_cache(const HeadsArgs& a, const uint8_t* codes, int second,
+                                         const float* scale) {
+    const auto inside = [&](const uint8_t* c, const float* s) {
+        return codes >= c && codes + second + 8 <= c + a.code_end && scale >= s &&
+               scale < s + a.scale_end;
+    };
+    return inside(a.k_codes, a.k_scales) || inside(a.v_codes, a.v_scales);
+}
+
 // A head's codes and scale into the cache: x and the largest magnitude of the
-// lane.
+// lane; the lane's codes go to `codes` and `second` further on.
 template <int G>
-__device__ __forceinline__ void store_codes(const HeadsArgs& a, float2 x[8], float m, bool store,
-                                            bool first_lane, uint8_t* codes, float* scales,
-                                            int64_t code_at, int64_t scale_at, int da, int db) {
-    m = head_max<G>(m);
-    const bool clamped = m > a.scale_ub;
-    m = fmaxf(fminf(m, a.scale_ub), 1e-12f);
+__device__ __forceinline__ void store_codes(const HeadsArgs& a, const float2 x[8], float m, bool store,
+                                            bool first_lane, uint8_t* codes, int second,
+                                            float* scale_out) {
     uint2 qa, qb;
-    const float scale = quantise(x, m, clamped, qa, qb);
-    if (store && RRF_IN_BOUNDS(code_at >= 0 && code_at + a.dim <= a.code_end && scale_at >= 0 &&
-                                   scale_at < a.scale_end,
-                               a.err)) {
-        *reinterpret_cast<uint2*>(codes + code_at + da) = qa;
-        *reinterpret_cast<uint2*>(codes + code_at + db) = qb;
-        if (first_lane) scales[scale_at] = scale;
+    const float scale = quantise(x, head_max<G>(m), a.scale_ub, qa, qb);
+    if (store && RRF_IN_BOUNDS(in_cache(a, codes, second, scale_out), a.err)) {
+        *reinterpret_cast<uint2*>(codes) = qa;
+        *reinterpret_cast<uint2*>(codes + second) = qb;
+        if (first_lane) *scale_out = scale;
     }
 }
 
@@ -337,8 +344,8 @@ __device__ __forceinline__ void work_chunks(const HeadsArgs& a, const Lane& l, c
     // the output, as bf16 or as codes and scales
     const HeadView& out = KIND == kQuery ? a.q_out : a.k_out;
     uint16_t* dst = out.p + l.token * out.token_stride + first * out.head_stride;
-    int64_t code_at = l.code_at + first * a.code_head;
-    int64_t scale_at = l.scale_at + first * a.scale_head;
+    uint8_t* codes = (KIND == kKey ? a.k_codes : a.v_codes) + l.code_at + first * a.code_head + da;
+    float* scales = (KIND == kKey ? a.k_scales : a.v_scales) + l.scale_at + first * a.scale_head;
 
 #pragma unroll 1
     for (; c < end; ++c, left -= kHeads) {
@@ -365,10 +372,9 @@ __device__ __forceinline__ void work_chunks(const HeadsArgs& a, const Lane& l, c
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
             }
-            store_codes<G>(a, x, m, left > 0, l.g == 0, KIND == kKey ? a.k_codes : a.v_codes,
-                           KIND == kKey ? a.k_scales : a.v_scales, code_at, scale_at, da, db);
-            code_at += kHeads * a.code_head;
-            scale_at += kHeads * a.scale_head;
+            store_codes<G>(a, x, m, left > 0, l.g == 0, codes, db - da, scales);
+            codes += kHeads * a.code_head;
+            scales += kHeads * a.scale_head;
         }
     }
 }
@@ -451,11 +457,11 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, kBlocksPerSm) heads_kerne
 // Keys and values as they are into the cache.  Nothing but its place belongs
 // to a token, so a warp keeps to one chunk (4 heads of 128, of the keys or of
 // the values) and takes `per` tokens: lane t works out the place of the
-// warp's token t, once for all.  (B200, 32768 tokens x 8 heads x 128: 35.0 us,
+// warp's token t, once for all.  (B200, 32768 tokens x 8 heads x 128: 36 us,
 // 89% of the copy rate; a warp for all the chunks of one token, which spends
 // a third of its instructions on the token's set-up, took 49 us.)
 template <int G>
-__global__ void __launch_bounds__(32 * kWarpsPerBlock) write_kernel(const HeadsArgs a) {
+__global__ void __launch_bounds__(32 * kWarpsPerBlock, kWriteBlocksCompiled) write_kernel(const HeadsArgs a) {
     constexpr int kHeads = 32 / G;
     __shared__ uint4 rings[kStages * kStageVecs];  // [stage][half][thread]
     __shared__ longlong2 places[kWarpsPerBlock][32];
@@ -500,9 +506,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) write_kernel(const HeadsA
         places[warp][lane] = p;
     }
     __syncwarp();
-    uint8_t* codes = key ? a.k_codes : a.v_codes;
-    float* scales = key ? a.k_scales : a.v_scales;
-    const int64_t code_head = head * a.code_head, scale_head = head * a.scale_head;
+    // (of a chunk's last heads, some may not be there: their lanes store nothing)
+    uint8_t* codes = (key ? a.k_codes : a.v_codes) + head * a.code_head + da;
+    float* scales = (key ? a.k_scales : a.v_scales) + head * a.scale_head;
 #pragma unroll 1
     for (int t = 0; t < n; ++t) {
         asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
@@ -514,8 +520,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) write_kernel(const HeadsA
         bf16x8_to_f32x2(rb, x + 4);
         feed();
         if (place.x < 0) continue;  // uniform in the warp
-        store_codes<G>(a, x, max_bf16x16(ra, rb), mine, l.g == 0, codes, scales,
-                       place.x + code_head, place.y + scale_head, da, db);
+        store_codes<G>(a, x, max_bf16x16(ra, rb), mine, l.g == 0, codes + place.x, db - da,
+                       scales + place.y);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }

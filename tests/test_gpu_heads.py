@@ -101,7 +101,8 @@ SHAPES = [  # tokens, q heads, kv heads, dim, rot
     (1, 8, 1, 128, 128), (2, 1, 1, 16, 16), (37, 12, 3, 80, 32), (5, 7, 7, 64, 64),
     (300, 8, 2, 128, 64), (3, 5, 1, 96, 96), (19, 3, 2, 192, 64), (33, 4, 4, 256, 256),
     (7, 2, 1, 272, 16), (4, 3, 3, 512, 512), (65, 9, 5, 48, 48), (11, 33, 17, 32, 16),
-    (6, 4, 2, 128, 0), (1000, 1, 1, 64, 32)]
+    (6, 4, 2, 128, 0), (1000, 1, 1, 64, 32), (23, 13, 7, 160, 96), (9, 11, 11, 144, 144),
+    (50, 21, 1, 48, 16), (4, 6, 6, 112, 112)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
