@@ -2483,38 +2483,54 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
 }
 
 // The products with an epilogue.  A persistent CTA (or pair) takes its tiles
-// in rounds, and a round's time is near a fixed part e plus the k-tiles times
-// c, whatever M and N.  Measured on B200 (us above the 3.7 of an empty call; N
-// = 256 .. 16384, M = 1 .. 4096, K = 1024 .. 7168, silu and residual):
-//   swapped, at most 8 / 16 / 32 rows  e 0 / 0 / 0.3  c 0.085 / 0.113 / 0.135
-//                       (MX: c 0.15 / 0.15 / 0.18)
-//   64 columns, 64-row A stages        e 0.3  c 0.24    (K % 128 != 0: c 0.35)
-//   64 columns, 128 rows               e 0.7  c 0.254   (K % 128 != 0: c 0.35)
-//   128 columns, 64-row A stages       e 1.5  c 0.26
-//   128 columns, 128 rows              e 2.0  c 0.2875
-//   256 x 256 on SM pairs              e 5.0  c 0.29
-//   K split, 32 / 64 / 128 rows        e 0 / 0.3 / 1.7  c 0.21 / 0.225 / 0.25
+// in rounds.  The first takes e + k-tiles * c, a further one e2 + k-tiles * c2
+// but at least what a tile's epilogue takes, which the products of the next
+// tile only hide.  Measured on B200 (us above the 3.7 of an empty call; N =
+// 256 .. 65536, M = 1 .. 4096, K = 128 .. 7168, silu and residual; K % 128 !=
+// 0: c 0.35 for 64 columns):
+//                                      e    c        further rounds
+//   swapped, at most  8 rows           0    0.085    0.95 + 0.085 k
+//                    16 rows           0    0.113    1.6 + 0.113 k
+//                    32 rows           0.3  0.135    3.0 + 0.135 k
+//                       (MX: c 0.15, 0.15, 0.18)
+//   64 columns, 64-row A stages        0.9  0.215    1.9 + 0.17 k, least 2.8
+//   128 columns, 64-row A stages       1.6  0.245    1.6 + 0.36 k, least 3.05
+//   64 columns, 128 rows               0.8  0.256    as the first, least 3.1
+//                       (MX: c 0.30)
+//   128 columns, 128 rows              1.7  0.32     as the first, least 4.2
+//                       (MX: e 1.5  c 0.38)
+//   256 x 256 on SM pairs              3.6  0.39     as the first, least 5.0
+//                       (MX: e 4.2  c 0.475)
+//   K split, 32 / 64 / 128 rows        0 / 0.3 / 1.7  0.21 / 0.225 / 0.25
 //                       of the k-tiles of one CTA, rounded up to its stages
 // (the operands that a CTA loads per k-tile count, hardly its products: 64
-// columns cost nearly as much as 128).  The kernel of the least rounds * (e +
-// k-tiles * c) is taken.  K is split among as many CTAs as are resident at
-// once (of clusters of 2, 4 and 8: 74, 32 and 15).  Against plan_scaled_mm's
-// choice: 64 x 1024 x 7168 7.2 (split in 4) for 15.6 us, 1 x 1024 x 7168 6.7
-// for 8.5, 128 x 2048 x 7168 9.6 for 18.3, 512 x 7168 x 4096 22.9 (pairs) for
-// 27.1, 256 x 7168 x 4096 16.7 (128 columns) for 21.6, 64 x 16384 x 7168 25.8
-// (128 columns) for 31.3, MX 1999 x 2576 x 1024 15.6 (128 columns) for 18.1.
+// columns cost nearly as much as 128).  No kernel is done before e and the
+// weight's bytes at 6 TB/s.  The kernel of the least cost is taken.  K is split
+// among as many CTAs as are resident at once (of clusters of 2, 4 and 8: 74,
+// 32 and 15).  Against plan_scaled_mm's choice: 64 x 1024 x 7168 7.2 (split in
+// 4) for 15.6 us, 1 x 1024 x 7168 6.7 for 8.5, 128 x 2048 x 7168 9.6 for 18.3,
+// 512 x 7168 x 4096 22.0 (pairs) for 27.3, 256 x 7168 x 4096 16.7 (128 columns)
+// for 21.6, 64 x 16384 x 7168 25.2 (128 columns) for 31.3, 1 x 24576 x 4096
+// 19.3 (swapped) for 26.7 (128 columns), 256 x 16384 x 256 9.0 (pairs) for 13.1
+// (64 columns), MX 1999 x 2576 x 1024 15.9 and 4096 x 4096 x 1024 33.9 (128
+// columns) for 18.1 and 36.2 (pairs).
 GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) {
-    GemmPlan best = plan_scaled_mm(M, N, K, mx, sm_count);
+    GemmPlan best;
     const bool atoms = K % kBK == 0;  // several k-tiles per box
     const int64_t ktiles = (K + kBK - 1) / kBK;
-    double least = 0.0;
-    auto offer = [&](const GemmPlan& p, double cost) {
-        if (least == 0.0 || cost < least) {
-            least = cost;
+    double lowest = -1.0;
+    auto offer = [&](const GemmPlan& p, double e, double cost) {
+        const double weight = e + (double)N * (double)K / 6.0e6;
+        if (cost < weight) cost = weight;
+        if (lowest < 0.0 || cost < lowest) {
+            lowest = cost;
             best = p;
         }
     };
-    auto offer_tile = [&](int kernel, int arows, int bn, int z, double e, double c) {
+    struct Rounds {
+        double e, c, e2, c2, least;
+    };
+    auto offer_tile = [&](int kernel, int arows, int bn, int z, const Rounds& r) {
         GemmPlan p;
         p.kernel = kernel;
         p.a_rows = arows;
@@ -2524,24 +2540,37 @@ GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_cou
         const int64_t units = kernel == kGemmPair ? sm_count / 2 : sm_count;
         p.tiles = ((M + rows - 1) / rows) * ((N + bn - 1) / bn);
         p.ctas = (p.tiles < units ? p.tiles : units) * (kernel == kGemmPair ? 2 : 1);
-        offer(p, (double)((p.tiles + units - 1) / units) * (e + (double)ktiles * c));
+        const double k = (double)ktiles, further = r.e2 + k * r.c2;
+        offer(p, r.e,
+              r.e + k * r.c +
+                  (double)((p.tiles - 1) / units) * (further > r.least ? further : r.least));
     };
-    if (best.kernel == kGemmSwap) {
-        const double c = M <= 8    ? (mx ? 0.15 : 0.085)
-                         : M <= 16 ? (mx ? 0.15 : 0.113)
-                                   : (mx ? 0.18 : 0.135);
-        const int64_t rounds = (best.tiles + sm_count - 1) / sm_count;
-        offer(best, (double)rounds * ((M > 16 ? 0.3 : 0.0) + (double)ktiles * c));
-    } else {
-        if (M <= 64) {
-            offer_tile(kGemmTile, 64, 64, atoms ? 4 : 1, 0.3, atoms ? 0.24 : 0.35);
-            if (atoms) offer_tile(kGemmTile, 64, 128, 2, 1.5, 0.26);
-        } else {
-            offer_tile(kGemmTile, kBM, 64, atoms ? 2 : 1, 0.7, atoms ? 0.254 : 0.35);
-        }
-        if (M > 64 || !atoms) offer_tile(kGemmTile, kBM, 128, 1, 2.0, 0.2875);
-        if (M > 128) offer_tile(kGemmPair, 256, 256, 1, 5.0, 0.29);
+    auto even = [](double e, double c, double least) { return Rounds{e, c, e, c, least}; };
+    if (M <= 32 && atoms) {
+        const int rows = M <= 8 ? 8 : M <= 16 ? 16 : 32;
+        const double c = rows == 8    ? (mx ? 0.15 : 0.085)
+                         : rows == 16 ? (mx ? 0.15 : 0.113)
+                                      : (mx ? 0.18 : 0.135);
+        offer_tile(kGemmSwap, rows, 64, rows == 8 && !mx ? 8 : 4,
+                   {rows == 32 ? 0.3 : 0.0, c, rows == 8    ? 0.95
+                                               : rows == 16 ? 1.6
+                                                            : 3.0,
+                    c, 0.0});
     }
+    if (M <= 64) {
+        offer_tile(kGemmTile, 64, 64, atoms ? 4 : 1,
+                   {0.9, atoms ? 0.215 : 0.35, 1.9, atoms ? 0.17 : 0.35, 2.8});
+        if (atoms) offer_tile(kGemmTile, 64, 128, 2, {1.6, 0.245, 1.6, 0.36, 3.05});
+    } else {
+        offer_tile(kGemmTile, kBM, 64, atoms ? 2 : 1,
+                   even(0.8, !atoms ? 0.35
+                             : mx   ? 0.30
+                                    : 0.256,
+                        3.1));
+    }
+    if (M > 64 || !atoms)
+        offer_tile(kGemmTile, kBM, 128, 1, even(mx ? 1.5 : 1.7, mx ? 0.38 : 0.32, 4.2));
+    if (M > 128) offer_tile(kGemmPair, 256, 256, 1, even(mx ? 4.2 : 3.6, mx ? 0.475 : 0.39, 5.0));
     if (atoms) {
         GemmPlan p;
         p.kernel = kGemmSplit;
@@ -2558,7 +2587,7 @@ GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_cou
             const int64_t split = 2 << i;
             if (p.tiles > resident[i] || groups < split) continue;  // (a CTA has a group at least)
             p.ctas = p.tiles * split;
-            offer(p, e + (double)((groups + split - 1) / split * p.k_tiles_per_stage) * c);
+            offer(p, e, e + (double)((groups + split - 1) / split * p.k_tiles_per_stage) * c);
         }
     }
     return best;

@@ -160,10 +160,13 @@ def test_scales_and_bias_of_any_alignment(rrf, m):
     assert torch.equal(call(rrf, p, "silu"), want)
 
 
-@pytest.mark.parametrize("m,n,k,mx", [(8, 16384, 1024, False), (32, 16384, 512, True),
-                                      (64, 10240, 512, False), (64, 37888, 1024, False),
-                                      (50, 37888, 1024, True),
-                                      (100, 10240, 256, True), (4096, 4096, 512, False),
+@pytest.mark.parametrize("m,n,k,mx", [(8, 16384, 1024, False), (1, 9488, 128, False),
+                                      (12, 14336, 256, True), (24, 18960, 2048, False),
+                                      (40, 18960, 4096, False), (24, 18960, 4096, True),
+                                      (64, 37888, 1024, False), (50, 37888, 1024, True),
+                                      (70, 18960, 256, True), (70, 18960, 128, False),
+                                      (2048, 2576, 1040, False), (700, 9488, 128, True),
+                                      (4096, 4096, 512, False),
                                       (4096, 4096, 512, True), (4096, 4096, 2048, False),
                                       (4096, 4096, 2048, True)])
 def test_several_tiles_of_a_block(rrf, m, n, k, mx):
