@@ -519,12 +519,12 @@ struct Tile {
     // an epilogue warp for each 32 rows and each 64 columns
     static constexpr int kEpiWarps = 4 * (BN / kChunk);
     static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
-    // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 8
-    // at 64, 12 with 64-row A stages, 3 with four k-tiles of 64 rows
     // with 64-row A stages only the first two quarters of the accumulator
     // hold rows, and only their warps have boxes
     static constexpr int kEpiAreas = AROWS == kBM || BN == kChunk ? kEpiWarps : kEpiWarps / 2;
     using Epi = EpiWarp<kEpiAreas, 1, true>;
+    // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 8
+    // at 64 (one k-tile), 4 with two k-tiles, 3 with four of 64 rows
     static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
     static constexpr int kStages = kBudget / kStageBytes > 12 ? 12 : kBudget / kStageBytes;
     static constexpr int kTmemCols = 2 * BN;  // two accumulators
@@ -1478,10 +1478,10 @@ struct MxTile {
     static constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
     static constexpr int kEpiWarps = 4 * (BN / kChunk);
     static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
-    // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 4
-    // at 64, 3 with four 64-row k-tiles
     static constexpr int kEpiAreas = AROWS == kBM || BN == kChunk ? kEpiWarps : kEpiWarps / 2;
     using Epi = EpiWarp<kEpiAreas, 1, false>;
+    // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 4
+    // at 64, 3 with four 64-row k-tiles
     static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
     static constexpr int kStages = kBudget / kStageStride > 12 ? 12 : kBudget / kStageStride;
     static constexpr int kAccCols = 2 * BN;          // two accumulators

@@ -29,8 +29,8 @@ namespace {
 
 constexpr int kWarpsPerBlock = 4;
 
-// Measured on B200 (8192 tokens x 72 heads x 128, norm and rotation; 302 MB in
-// 51.4 us, 91% of the copy rate).  The first form loaded a warp's chunks into
+// Measured on B200 (8192 tokens x 72 heads x 128, norm and rotation; 306 MB in
+// 51.2 us, 91% of the copy rate).  The first form loaded a warp's chunks into
 // registers: 112 of them a thread, 16 warps an SM, 87 us.  Copies into a ring
 // of shared memory, which hold no registers, keep 3 chunks of each warp in
 // flight: 52 us.
@@ -90,7 +90,7 @@ __device__ __forceinline__ float fast_reciprocal(float v) {
 // about half an ulp.  Rows above 1e30 are scaled by 2^-64 first, so that n
 // stays finite.  Values beyond a bound (scale_ub) saturate; only where they are
 // 1e30 times the bound, and y might not be finite, is it left uncorrected.
-// (Cutting x to the bound instead cost every row 20 of 185 instructions.)
+// (Cutting x to the bound instead costs every row some 20 instructions.)
 __device__ __forceinline__ float quantise(const float2 x[8], float most, float scale_ub, uint2& qa,
                                           uint2& qb) {
     const float m = fmaxf(fminf(most, scale_ub), 1e-12f);
@@ -290,8 +290,8 @@ __device__ __forceinline__ void feed_next(const HeadsArgs& a, const Lane& l, Fee
                             RRF_IN_BOUNDS(8 * l.vb + 8 <= a.dim && l.token < a.tokens, a.err);
         const uint16_t* p = wanted ? f.src : a.k.p;  // (nothing is read)
         copy16(f.ring + f.stage * (kStageVecs * 16), p, wanted);
-        copy16(f.ring + f.stage * (kStageVecs * 16) + kStageVecs * 8, p + (wanted ? 8 * (l.vb - l.va) : 0),
-               wanted);
+        copy16(f.ring + f.stage * (kStageVecs * 16) + kStageVecs * 8,
+               p + (wanted ? 8 * (l.vb - l.va) : 0), wanted);
         f.src += f.step;
         f.head += 32 / G;
         --f.left;
@@ -303,8 +303,9 @@ __device__ __forceinline__ void feed_next(const HeadsArgs& a, const Lane& l, Fee
 
 // (the bounds-checking build) Eight codes at `codes` and `second` further on,
 // and a scale, lie in the keys' or the values' arrays.
-[[maybe_unused]] __device__ __forceinline__ bool in_cache(const HeadsArgs& a, const uint8_t* codes, int second,
-                                         const float* scale) {
+[[maybe_unused]] __device__ __forceinline__ bool in_cache(const HeadsArgs& a,
+                                                          const uint8_t* codes, int second,
+                                                          const float* scale) {
     const auto inside = [&](const uint8_t* c, const float* s) {
         return codes >= c && codes + second + 8 <= c + a.code_end && scale >= s &&
                scale < s + a.scale_end;
@@ -315,9 +316,9 @@ __device__ __forceinline__ void feed_next(const HeadsArgs& a, const Lane& l, Fee
 // A head's codes and scale into the cache: x and the largest magnitude of the
 // lane; the lane's codes go to `codes` and `second` further on.
 template <int G>
-__device__ __forceinline__ void store_codes(const HeadsArgs& a, const float2 x[8], float m, bool store,
-                                            bool first_lane, uint8_t* codes, int second,
-                                            float* scale_out) {
+__device__ __forceinline__ void store_codes(const HeadsArgs& a, const float2 x[8], float m,
+                                            bool store, bool first_lane, uint8_t* codes,
+                                            int second, float* scale_out) {
     uint2 qa, qb;
     const float scale = quantise(x, head_max<G>(m), a.scale_ub, qa, qb);
     if (store && RRF_IN_BOUNDS(in_cache(a, codes, second, scale_out), a.err)) {
@@ -461,7 +462,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, kBlocksPerSm) heads_kerne
 // 89% of the copy rate; a warp for all the chunks of one token, which spends
 // a third of its instructions on the token's set-up, took 49 us.)
 template <int G>
-__global__ void __launch_bounds__(32 * kWarpsPerBlock, kWriteBlocksCompiled) write_kernel(const HeadsArgs a) {
+__global__ void __launch_bounds__(32 * kWarpsPerBlock, kWriteBlocksCompiled)
+    write_kernel(const HeadsArgs a) {
     constexpr int kHeads = 32 / G;
     __shared__ uint4 rings[kStages * kStageVecs];  // [stage][half][thread]
     __shared__ longlong2 places[kWarpsPerBlock][32];

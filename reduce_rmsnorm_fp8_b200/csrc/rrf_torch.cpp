@@ -62,6 +62,12 @@ int64_t integer(PyObject* o) {
     return v;
 }
 
+int truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused("a truth value is wanted");
+    return v;
+}
+
 bool on(const at::Tensor& t, int index) { return t.is_cuda() && t.get_device() == index; }
 
 // A dense vector of n values (any shape).
@@ -192,7 +198,7 @@ struct Norm {
         k_gamma = vector(tensor(v[1], "k_gamma"), "k_gamma", at::kBFloat16, dim, index);
         eps = (float)number(v[2]);
         weight_offset = (float)number(v[3]);
-        interleaved = PyObject_IsTrue(v[6]);
+        interleaved = truth(v[6]);
         const at::Tensor& table = optional(v[4], "cos_sin");
         if (!table.defined()) return;
         need(table.scalar_type() == at::kFloat && table.dim() == 2 && table.size(1) > 0 &&

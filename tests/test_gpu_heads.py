@@ -541,6 +541,8 @@ def test_refusals_of_tensors(rrf):
         with pytest.raises(ValueError, match="cache|scales" if name[1:] in ("_cache", "_scales")
                            else name):
             rrf.rrf_qk_norm_rope_kv_cache_fp8(**{**args, name: bad})
+    with pytest.raises(RuntimeError, match="ambiguous"):  # (no truth value)
+        rrf.rrf_qk_norm_rope_kv_cache_fp8(**args, interleaved=torch.zeros(2))
     with pytest.raises(rrf.RrfError) as e:
         rrf.rrf_qk_norm_rope_kv_cache_fp8(**{**args, "eps": -1.0})
     assert e.value.status == rrf.Status.ERR_VALUE
