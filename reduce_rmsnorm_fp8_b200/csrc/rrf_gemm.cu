@@ -17,9 +17,9 @@
 //            a cluster; per-token and MX forms (only the calls with an
 //            epilogue, see plan_scaled_mm_act).
 // A persistent CTA per SM walks 128 x BN tiles of out (BN 128 or 64).
-// Warp roles (the same in every kernel; the swapped kernel's MX form adds a
-// seventh warp that rearranges the scale codes of each stage, and tiles of 128
-// columns have eight epilogue warps, those of 256 sixteen):
+// Warp roles (the same in every kernel; the swapped and the split kernels have
+// four epilogue warps, the swapped kernel's MX form a seventh warp that
+// rearranges the scale codes of each stage):
 //   warp 0   one thread issues the TMA loads of the A (128 x 128 bytes) and
 //            B (BN x 128 bytes) k-tiles into a ring of shared-memory stages
 //            (128-byte swizzle, the layout the MMA descriptors name);
@@ -28,7 +28,8 @@
 //            M = 128, N = BN, K = 32 per instruction, 4 per k-tile); a
 //            tcgen05.commit per k-tile hands the stage back to the producer,
 //            one per tile hands the accumulator to the epilogue;
-//   warps 2-5 the epilogue: tcgen05.ld of its 32 accumulator lanes (rows),
+//   warps 2-17 the epilogue: tcgen05.ld of its 32 accumulator lanes (rows) and
+//            a quarter of the tile's columns,
 //            the two scales, bias, activation and residual, one rounding to
 //            bf16, boxes taken out by TMA stores, while the MMAs of the next
 //            tile fill the other accumulator.
@@ -306,14 +307,15 @@ __device__ __forceinline__ void activate_all(int act, float2 y[PAIRS]) {
     else activate_pairs<RRF_ACT_GELU_TANH, PAIRS>(y);
 }
 
-// The epilogue of a warp's 32 rows (one accumulator lane each), 64 columns (a
-// chunk) at a time.  A lane holds a row, but memory is read and written in
-// boxes of 32 rows x 128 bytes: a TMA load brings the residual's box into
-// shared memory a chunk ahead, each lane adds its row to it in place, and a
-// TMA store takes the box out (rows and columns past the matrix are not
-// written).  Boxes are 128-byte swizzled: 16-byte piece p of row r sits at
-// p ^ (r % 8), so that a column of rows does not meet in a bank.  The scales
-// and the bias of the chunk's columns are loaded a chunk ahead too.
+// The epilogue of a warp's 32 rows (one accumulator lane each) and a quarter of
+// the tile's columns (a chunk: 64, 32 or 16).  A lane holds a row, but memory is
+// read and written in boxes of 32 rows x a chunk: a TMA load brings the
+// residual's box into shared memory a chunk ahead, each lane adds its row to it
+// in place, and a TMA store takes the box out (rows and columns past the matrix
+// are not written).  Boxes are swizzled over their rows' 128, 64 or 32 bytes
+// (16-byte piece p of row r at p ^ r % 8, p ^ r / 2 % 4 or p ^ r / 4 % 2), so
+// that a column of rows does not meet in a bank.  The scales and the bias of the
+// chunk's columns are loaded a chunk ahead too.
 // B200, 4096 x 4096 x 1024 with silu and residual: 88.9 us with each lane
 // reading and writing its own row 64 bytes at a time and its column scales one
 // by one; 35.1 us through shared memory with the warp's own coalesced loads
@@ -321,17 +323,19 @@ __device__ __forceinline__ void activate_all(int act, float2 y[PAIRS]) {
 // (The products alone take 15 us there: at so short a K the epilogue's
 // shared-memory traffic, 5 passes over 64 KB a tile, meets the operands' in the
 // same banks.  At 8192^3 the power limit bounds both: 1.4 GHz, 452 us without
-// and 484 with gelu and residual.)
-constexpr int kChunk = 64;               // columns of a chunk
-constexpr int kBoxBytes = 32 * kChunk * 2;
+// and 484 with gelu and residual.)  Sixteen warps for the smaller tiles as well,
+// against a warp for each 64 columns: 64 x 4096 x 512 5.5 -> 4.7 us, 1024 x 1024
+// x 1024 6.8 -> 6.1.
+constexpr int kPairChunk = 64;  // columns of a chunk, on SM pairs
 
 // Of `warps` epilogue warps with `boxes` boxes each: the boxes (1024-byte
 // aligned), per warp a (scale, scale, bias, bias) for each pair of columns,
 // and per box a barrier.
-template <int WARPS, int BOXES>
+template <int WARPS, int BOXES, int CHUNK>
 struct EpiLayout {
+    static constexpr int kBoxBytes = 32 * CHUNK * 2;
     static constexpr int kColumns = WARPS * BOXES * kBoxBytes;
-    static constexpr int kBarriers = kColumns + WARPS * kChunk * 8;
+    static constexpr int kBarriers = kColumns + WARPS * CHUNK * 8;
     static constexpr int kBytes = kBarriers + WARPS * BOXES * 8;
 };
 
@@ -350,9 +354,11 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // One epilogue warp: chunk() works on the chunks of its tiles in turn.
-template <int WARPS, int BOXES, bool SCALED>
+template <int WARPS, int BOXES, bool SCALED, int CHUNK>
 struct EpiWarp {
-    using L = EpiLayout<WARPS, BOXES>;
+    using L = EpiLayout<WARPS, BOXES, CHUNK>;
+    static constexpr int kBoxBytes = L::kBoxBytes;
+    static constexpr int kPieces = CHUNK / 8;  // 16-byte pieces of a box's row
     const GemmArgs& g;
     const CUtensorMap* res_map;
     const CUtensorMap* out_map;
@@ -367,7 +373,7 @@ struct EpiWarp {
     __device__ __forceinline__ EpiWarp(const GemmArgs& args, const CUtensorMap* rm,
                                        const CUtensorMap* om, uint8_t* area, int warp, int l)
         : g(args), res_map(rm), out_map(om), boxes(area + warp * BOXES * kBoxBytes),
-          columns(reinterpret_cast<float4*>(area + L::kColumns + warp * kChunk * 8)),
+          columns(reinterpret_cast<float4*>(area + L::kColumns + warp * CHUNK * 8)),
           bars(reinterpret_cast<uint64_t*>(area + L::kBarriers) + warp * BOXES), lane(l),
           count(0), loading(false), scale(both(1.0f)), bias(both(-0.0f)) {}
 
@@ -410,16 +416,16 @@ struct EpiWarp {
             return true;
         }
         ++count;
-        columns[lane] = make_float4(scale.x, scale.y, bias.x, bias.y);
+        if (lane < CHUNK / 2) columns[lane] = make_float4(scale.x, scale.y, bias.x, bias.y);
         __syncwarp();
         if (more) load_columns(n_next);
         // 16 columns at a time, in a loop: the block's many warps hide one
         // another's latency, and the code stays short
 #pragma unroll 1
-        for (int h = 0; h < kChunk / 16; ++h) {
+        for (int h = 0; h < CHUNK / 16; ++h) {
             float v[16];
             tmem_load_cols<16>(taddr + 16 * h, v);
-            if (h == kChunk / 16 - 1) after_read();
+            if (h == CHUNK / 16 - 1) after_read();
             float2 y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -430,9 +436,10 @@ struct EpiWarp {
                 y[i] = __fadd2_rn(y[i], make_float2(s.z, s.w));
             }
             activate_all<8>(g.act, y);
-            uint4* row = box + lane * 8;
-            uint4& lo = row[(2 * h) ^ (lane & 7)];
-            uint4& hi = row[(2 * h + 1) ^ (lane & 7)];
+            uint4* row = box + lane * kPieces;
+            const int turn = kPieces == 8 ? lane & 7 : kPieces == 4 ? (lane >> 1) & 3 : (lane >> 2) & 1;  // (the swizzle)
+            uint4& lo = row[(2 * h) ^ turn];
+            uint4& hi = row[(2 * h + 1) ^ turn];
             if (g.residual != nullptr) {
                 float2 r[8];
                 bf16x8_to_f32x2(lo, r);
@@ -484,7 +491,7 @@ struct EpiWarp {
     // (a bias that is not there is -0, which leaves every value as it is)
     __device__ __forceinline__ void load_columns(int n) {
         const int col = n + 2 * lane;
-        if (col >= g.N) return;  // (N is even)
+        if (lane >= CHUNK / 2 || col >= g.N) return;  // (N is even)
         if constexpr (SCALED) scale = make_float2(g.b_scale[col], g.b_scale[col + 1]);
         if (g.bias != nullptr)
             bias = make_float2(__uint_as_float((uint32_t)g.bias[col] << 16),
@@ -516,13 +523,14 @@ struct Tile {
     static constexpr int kBBytes = BN * kBK;           // one k-tile of B
     static constexpr int kBOffset = Z * kABytes;       // B tiles follow the Z A tiles
     static constexpr int kStageBytes = Z * (kABytes + kBBytes);
-    // an epilogue warp for each 32 rows and each 64 columns
-    static constexpr int kEpiWarps = 4 * (BN / kChunk);
+    // an epilogue warp for each 32 rows and each quarter of the columns
+    static constexpr int kChunk = BN / 4;
+    static constexpr int kEpiWarps = 16;
     static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
     // with 64-row A stages only the first two quarters of the accumulator
     // hold rows, and only their warps have boxes
-    static constexpr int kEpiAreas = AROWS == kBM || BN == kChunk ? kEpiWarps : kEpiWarps / 2;
-    using Epi = EpiWarp<kEpiAreas, 1, true>;
+    static constexpr int kEpiAreas = AROWS == kBM ? kEpiWarps : kEpiWarps / 2;
+    using Epi = EpiWarp<kEpiAreas, 1, true, kChunk>;
     // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 8
     // at 64 (one k-tile), 4 with two k-tiles, 3 with four of 64 rows
     static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
@@ -687,9 +695,9 @@ __global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
         __syncwarp();
     } else {
         // ---- epilogue: warp w reads accumulator lanes 32 * (w % 4) ... and
-        // 64 columns
-        const int quarter = warp & 3, c = ((warp - 2) >> 2) * kChunk;
-        const int area = T::kEpiAreas == T::kEpiWarps ? warp - 2 : 2 * (c / kChunk) + (quarter & 1);
+        // a quarter of the columns
+        const int quarter = warp & 3, c = ((warp - 2) >> 2) * T::kChunk;
+        const int area = T::kEpiAreas == T::kEpiWarps ? warp - 2 : 2 * (c / T::kChunk) + (quarter & 1);
         typename T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, area, lane);
         int row0 = (blockIdx.x / tiles_n) * kBM + quarter * 32, n = (blockIdx.x % tiles_n) * BN + c;
         epi.ahead(row0, n);
@@ -1276,7 +1284,7 @@ struct PairTile {
     static constexpr int kStages = kPairStages;             // 128 KB
     static constexpr int kTmemCols = 512;                   // two 256-column accumulators
     static constexpr int kBarriers = 2 * kStages + 4 + 1;
-    using Epi = EpiWarp<kPairEpiWarps, kPairBoxes, true>;
+    using Epi = EpiWarp<kPairEpiWarps, kPairBoxes, true, kPairChunk>;
     static constexpr int kEpiOffset = kStages * kStageBytes;
     static constexpr int kBarrierOffset = kEpiOffset + Epi::L::kBytes;
     static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
@@ -1409,7 +1417,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                               peer_smem(&acc_empty[1], 0)};
         int tm, tn;
         grouped_tile(pair, tiles_m, tiles_n, tm, tn);
-        int row0 = tm * 256 + (int)rank * 128 + quarter * 32, n0 = tn * 256 + group * kChunk;
+        int row0 = tm * 256 + (int)rank * 128 + quarter * 32, n0 = tn * 256 + group * kPairChunk;
         epi.ahead(row0, n0);
         int j = 0;
         for (int t = pair; t < tiles; t += npairs, ++j) {
@@ -1417,12 +1425,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const bool more = t + npairs < tiles;
             if (more) grouped_tile(t + npairs, tiles_m, tiles_n, tm, tn);
             const int row_next = tm * 256 + (int)rank * 128 + quarter * 32;
-            const int n_next = tn * 256 + group * kChunk;
+            const int n_next = tn * 256 + group * kPairChunk;
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
             if (!__all_sync(0xFFFFFFFFu, have)) break;
             tc_fence_after_sync();
             const float sa = row0 + lane < g.M ? g.a_scale[row0 + lane] : 0.0f;
-            const uint32_t base = tmem + (uint32_t)(buf * BN + group * kChunk) +
+            const uint32_t base = tmem + (uint32_t)(buf * BN + group * kPairChunk) +
                                   ((uint32_t)(quarter * 32) << 16);
             if (!epi.chunk(base, sa, row0, n0, more, row_next, n_next, [&]() {
                     tc_fence_before_sync();
@@ -1476,10 +1484,11 @@ struct MxTile {
     static constexpr int kSfbOffset = kSfaOffset + Z * kSfBytes;
     static constexpr int kStageBytes = Z * (kABytes + kBBytes + 2 * kSfBytes);
     static constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-    static constexpr int kEpiWarps = 4 * (BN / kChunk);
+    static constexpr int kChunk = BN / 4;
+    static constexpr int kEpiWarps = 16;
     static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
-    static constexpr int kEpiAreas = AROWS == kBM || BN == kChunk ? kEpiWarps : kEpiWarps / 2;
-    using Epi = EpiWarp<kEpiAreas, 1, false>;
+    static constexpr int kEpiAreas = AROWS == kBM ? kEpiWarps : kEpiWarps / 2;
+    using Epi = EpiWarp<kEpiAreas, 1, false, kChunk>;
     // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 4
     // at 64, 3 with four 64-row k-tiles
     static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
@@ -1628,8 +1637,8 @@ __global__ void __launch_bounds__(MxTile<BN, AROWS, Z>::kThreadsPerCta, 1)
         __syncwarp();
     } else {
         // ---- epilogue: the scales are inside the accumulator
-        const int quarter = warp & 3, c = ((warp - 2) >> 2) * kChunk;
-        const int area = T::kEpiAreas == T::kEpiWarps ? warp - 2 : 2 * (c / kChunk) + (quarter & 1);
+        const int quarter = warp & 3, c = ((warp - 2) >> 2) * T::kChunk;
+        const int area = T::kEpiAreas == T::kEpiWarps ? warp - 2 : 2 * (c / T::kChunk) + (quarter & 1);
         typename T::Epi epi(g, &tma_res, &tma_out, smem + T::kEpiOffset, area, lane);
         int row0 = (blockIdx.x / tiles_n) * kBM + quarter * 32, n = (blockIdx.x % tiles_n) * BN + c;
         epi.ahead(row0, n);
@@ -1961,7 +1970,7 @@ struct MxPairTile {
     static constexpr uint32_t kSfbCol = kSfaCol + 4;             // 484 .. 491
     // full / empty per stage, full / empty per accumulator, overlap, drain
     static constexpr int kBarriers = 2 * kStages + 4 + 1 + 1;
-    using Epi = EpiWarp<kPairEpiWarps, kPairBoxes, false>;
+    using Epi = EpiWarp<kPairEpiWarps, kPairBoxes, false, kPairChunk>;
     static constexpr int kEpiOffset = kStages * kStageStride;
     static constexpr int kBarrierOffset = kEpiOffset + Epi::L::kBytes;
     static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
@@ -2110,7 +2119,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t leader_ovl_free = peer_smem(ovl_free, 0);
         int tm, tn;
         grouped_tile(pair, tiles_m, tiles_n, tm, tn);
-        int row0 = tm * 256 + (int)rank * 128 + quarter * 32, n0 = tn * 256 + group * kChunk;
+        int row0 = tm * 256 + (int)rank * 128 + quarter * 32, n0 = tn * 256 + group * kPairChunk;
         epi.ahead(row0, n0);
         int j = 0;
         for (int t = pair; t < tiles; t += npairs, ++j) {
@@ -2118,11 +2127,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const bool more = t + npairs < tiles;
             if (more) grouped_tile(t + npairs, tiles_m, tiles_n, tm, tn);
             const int row_next = tm * 256 + (int)rank * 128 + quarter * 32;
-            const int n_next = tn * 256 + group * kChunk;
+            const int n_next = tn * 256 + group * kPairChunk;
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
             if (!__all_sync(0xFFFFFFFFu, have)) break;
             tc_fence_after_sync();
-            const uint32_t base = tmem + (buf ? T::kBuf1 : 0u) + (uint32_t)(group * kChunk) +
+            const uint32_t base = tmem + (buf ? T::kBuf1 : 0u) + (uint32_t)(group * kPairChunk) +
                                   ((uint32_t)(quarter * 32) << 16);
             if (!epi.chunk(base, 1.0f, row0, n0, more, row_next, n_next, [&]() {
                     tc_fence_before_sync();
@@ -2243,26 +2252,29 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int b
            CUDA_SUCCESS;
 }
 
-// The bf16 output or residual [M, N] in the epilogue's boxes (kChunk columns x
+// The bf16 output or residual [M, N] in the epilogue's boxes (`chunk` columns x
 // 32 rows, 128-byte swizzle).
-bool make_box_map(CUtensorMap* map, const void* base, const GemmArgs& g) {
+bool make_box_map(CUtensorMap* map, const void* base, const GemmArgs& g, int chunk) {
     EncodeTiled fn = encode_tiled();
     if (fn == nullptr) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M};
     const cuuint64_t strides[1] = {(cuuint64_t)g.N * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kChunk, 32};
+    const cuuint32_t box[2] = {(cuuint32_t)chunk, 32};
     const cuuint32_t elem[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box,
-              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, 
+              chunk == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+              : chunk == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                            : CU_TENSOR_MAP_SWIZZLE_32B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }
 
 // The epilogue's maps: the residual's is the output's where there is none (or
 // where it is the output), and then not read.
-bool make_epilogue_maps(CUtensorMap* res, CUtensorMap* out, const GemmArgs& g) {
-    if (!make_box_map(out, g.out, g)) return false;
-    if (g.residual != nullptr && g.residual != g.out) return make_box_map(res, g.residual, g);
+bool make_epilogue_maps(CUtensorMap* res, CUtensorMap* out, const GemmArgs& g, int chunk) {
+    if (!make_box_map(out, g.out, g, chunk)) return false;
+    if (g.residual != nullptr && g.residual != g.out) return make_box_map(res, g.residual, g, chunk);
     *res = *out;
     return true;
 }
@@ -2313,7 +2325,7 @@ cudaError_t launch_bn(const GemmArgs& g, const void* a, const void* b, int sm_co
                       cudaStream_t stream) {
     using T = Tile<BN, AROWS, Z>;
     CUtensorMap ma, mb, mr, mo;
-    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z) || !make_epilogue_maps(&mr, &mo, g))
+    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z) || !make_epilogue_maps(&mr, &mo, g, T::kChunk))
         return cudaErrorInvalidValue;
     constexpr auto kernel = scaled_mm_kernel<BN, AROWS, Z>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
@@ -2347,7 +2359,7 @@ cudaError_t launch_pair(const GemmArgs& g, const void* a, const void* b, int sm_
     using T = PairTile;
     CUtensorMap ma, mb, mr, mo;
     if (!make_map(&ma, a, g.M, g.K, 128) || !make_map(&mb, b, g.N, g.K, 128) ||
-        !make_epilogue_maps(&mr, &mo, g))
+        !make_epilogue_maps(&mr, &mo, g, kPairChunk))
         return cudaErrorInvalidValue;
     const cudaError_t e = enable_dynamic_smem<scaled_mm_pair_kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -2361,7 +2373,7 @@ cudaError_t launch_mx(const GemmArgs& g, const void* a, const void* b, const uin
                       const uint8_t* sfb, int sm_count, cudaStream_t stream) {
     using T = MxTile<BN, AROWS, Z>;
     CUtensorMap ma, mb, mr, mo;
-    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z) || !make_epilogue_maps(&mr, &mo, g))
+    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z) || !make_epilogue_maps(&mr, &mo, g, T::kChunk))
         return cudaErrorInvalidValue;
     constexpr auto kernel = scaled_mm_mx_kernel<BN, AROWS, Z>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
@@ -2415,7 +2427,7 @@ cudaError_t launch_mx_pair(const GemmArgs& g, const void* a, const void* b, cons
     CUtensorMap ma, mb, msa, msb, mr, mo;
     if (!make_map(&ma, a, g.M, g.K, 128) || !make_map(&mb, b, g.N, g.K, 128) ||
         !make_sf_map(&msa, sfa, g.M, g.K, 1) || !make_sf_map(&msb, sfb, g.N, g.K, 2) ||
-        !make_epilogue_maps(&mr, &mo, g))
+        !make_epilogue_maps(&mr, &mo, g, kPairChunk))
         return cudaErrorInvalidValue;
     const cudaError_t e = enable_dynamic_smem<scaled_mm_mx_pair_kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -2493,14 +2505,16 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
 //                    16 rows           0    0.113    1.6 + 0.113 k
 //                    32 rows           0.3  0.135    3.0 + 0.135 k
 //                       (MX: c 0.15, 0.15, 0.18)
-//   64 columns, 64-row A stages        0.9  0.215    1.9 + 0.17 k, least 2.8
-//   128 columns, 64-row A stages       1.6  0.245    1.6 + 0.36 k, least 3.05
-//   64 columns, 128 rows               0.8  0.256    as the first, least 3.1
-//                       (MX: c 0.30)
-//   128 columns, 128 rows              1.7  0.32     as the first, least 4.2
-//                       (MX: e 1.5  c 0.38)
-//   256 x 256 on SM pairs              3.6  0.39     as the first, least 5.0
-//                       (MX: e 4.2  c 0.475)
+//   64 columns, 64-row A stages        0.4  0.195    1.2 + 0.235 k, least 2.0
+//                       (MX: c 0.255, 0.255)
+//   128 columns, 64-row A stages       1.1  0.245    1.5 + 0.36 k, least 2.6
+//                       (MX: c 0.31)
+//   64 columns, 128 rows               0.4  0.245    0.7 + 0.245 k, least 2.3
+//                       (MX: c 0.31)
+//   128 columns, 128 rows              1.2  0.31     1.5 + 0.33 k, least 3.1
+//                       (MX: c 0.37, 1.1 + 0.37 k)
+//   256 x 256 on SM pairs              4.3  0.35     3.5 + 0.45 k, least 4.9
+//                       (MX: 4.0 + 0.44 k, 5.6 + 0.43 k)
 //   K split, 32 / 64 / 128 rows        0 / 0.3 / 1.7  0.21 / 0.225 / 0.25
 //                       of the k-tiles of one CTA, rounded up to its stages
 // (the operands that a CTA loads per k-tile count, hardly its products: 64
@@ -2511,8 +2525,8 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
 // 4) for 15.6 us, 1 x 1024 x 7168 6.7 for 8.5, 128 x 2048 x 7168 9.6 for 18.3,
 // 512 x 7168 x 4096 22.0 (pairs) for 27.3, 256 x 7168 x 4096 16.7 (128 columns)
 // for 21.6, 64 x 16384 x 7168 25.2 (128 columns) for 31.3, 1 x 24576 x 4096
-// 19.3 (swapped) for 26.7 (128 columns), 256 x 16384 x 256 9.0 (pairs) for 13.1
-// (64 columns), MX 1999 x 2576 x 1024 15.9 and 4096 x 4096 x 1024 33.9 (128
+// 19.3 (swapped) for 26.7 (128 columns), 256 x 16384 x 256 8.7 (128 columns) for
+// 13.1 (64), MX 1999 x 2576 x 1024 15.7 and 4096 x 4096 x 1024 32.0 (128
 // columns) for 18.1 and 36.2 (pairs).
 GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) {
     GemmPlan best;
@@ -2545,7 +2559,6 @@ GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_cou
               r.e + k * r.c +
                   (double)((p.tiles - 1) / units) * (further > r.least ? further : r.least));
     };
-    auto even = [](double e, double c, double least) { return Rounds{e, c, e, c, least}; };
     if (M <= 32 && atoms) {
         const int rows = M <= 8 ? 8 : M <= 16 ? 16 : 32;
         const double c = rows == 8    ? (mx ? 0.15 : 0.085)
@@ -2559,18 +2572,20 @@ GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_cou
     }
     if (M <= 64) {
         offer_tile(kGemmTile, 64, 64, atoms ? 4 : 1,
-                   {0.9, atoms ? 0.215 : 0.35, 1.9, atoms ? 0.17 : 0.35, 2.8});
-        if (atoms) offer_tile(kGemmTile, 64, 128, 2, {1.6, 0.245, 1.6, 0.36, 3.05});
+                   atoms ? Rounds{0.4, mx ? 0.255 : 0.195, 1.2, mx ? 0.255 : 0.235, 2.0}
+                         : Rounds{0.4, 0.35, 0.4, 0.35, 2.0});
+        if (atoms) offer_tile(kGemmTile, 64, 128, 2, {1.1, mx ? 0.31 : 0.245, 1.5, 0.36, 2.6});
     } else {
-        offer_tile(kGemmTile, kBM, 64, atoms ? 2 : 1,
-                   even(0.8, !atoms ? 0.35
-                             : mx   ? 0.30
-                                    : 0.256,
-                        3.1));
+        const double c = !atoms ? 0.35 : mx ? 0.31 : 0.245;
+        offer_tile(kGemmTile, kBM, 64, atoms ? 2 : 1, {0.4, c, 0.7, c, 2.3});
     }
-    if (M > 64 || !atoms)
-        offer_tile(kGemmTile, kBM, 128, 1, even(mx ? 1.5 : 1.7, mx ? 0.38 : 0.32, 4.2));
-    if (M > 128) offer_tile(kGemmPair, 256, 256, 1, even(mx ? 4.2 : 3.6, mx ? 0.475 : 0.39, 5.0));
+    if (M > 64 || !atoms) {
+        offer_tile(kGemmTile, kBM, 128, 1,
+                   mx ? Rounds{1.2, 0.37, 1.1, 0.37, 3.1} : Rounds{1.2, 0.31, 1.5, 0.33, 3.1});
+    }
+    if (M > 128)
+        offer_tile(kGemmPair, 256, 256, 1,
+                   mx ? Rounds{4.0, 0.44, 5.6, 0.43, 0.0} : Rounds{4.3, 0.35, 3.5, 0.45, 4.9});
     if (atoms) {
         GemmPlan p;
         p.kernel = kGemmSplit;

@@ -114,7 +114,7 @@ MX = [(1, 256, 128, "swap", 8, 64), (16, 208, 512, "swap", 16, 64),
       (29, 7168, 1664, "swap", 32, 64), (60, 1040, 384, "tile", 64, 64),
       (33, 16400, 640, "tile", 64, 128), (200, 272, 384, "tile", 128, 64),
       (800, 2320, 1024, "tile", 128, 128), (500, 7168, 2048, "pair", 256, 256),
-      (2000, 8208, 1152, "pair", 256, 256),
+      (2000, 8208, 2176, "pair", 256, 256),
       (20, 4624, 1536, "split", 32, 2), (2, 2000, 2176, "split", 32, 4),
       (32, 912, 4224, "split", 32, 8), (64, 4624, 1664, "split", 64, 2),
       (40, 1104, 3200, "split", 64, 4), (33, 336, 7168, "split", 64, 8),
@@ -161,7 +161,7 @@ def test_scales_and_bias_of_any_alignment(rrf, m):
 
 
 @pytest.mark.parametrize("m,n,k,mx", [(8, 16384, 1024, False), (1, 9488, 128, False),
-                                      (12, 14336, 256, True), (24, 18960, 2048, False),
+                                      (12, 18960, 128, True), (24, 16384, 4096, False),
                                       (40, 18960, 4096, False), (24, 18960, 4096, True),
                                       (64, 37888, 1024, False), (50, 37888, 1024, True),
                                       (70, 18960, 256, True), (70, 18960, 128, False),
