@@ -559,7 +559,8 @@ cudaError_t launch_lanes(HeadsArgs a, bool norm, int sm_count, cudaStream_t stre
     const int64_t resident = (int64_t)sm_count * (norm ? kBlocksPerSm : kWriteBlocksPerSm);
     const int most = norm ? a.chunks : 32;  // (a write warp's lanes hold its places)
     double least = 0.0;
-    for (int units = most, parts = 1; units >= 1; ++parts) {
+    // (one round even with one unit to a warp: no split is cheaper)
+    for (int units = blocks_of(1) <= resident ? 1 : most, parts = 1; units >= 1; ++parts) {
         const int64_t rounds = (blocks_of(units) + resident - 1) / resident;
         const double cost = (double)rounds * (units + kSetUp);
         if (least == 0.0 || cost < least) {
