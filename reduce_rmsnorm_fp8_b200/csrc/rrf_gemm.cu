@@ -512,7 +512,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // rows x Z atoms of 128 values of K).  A TMA operation moves a few KB at a
 // fixed cost, and a CTA streams a weight only as fast as it issues them:
 // short, wide products (a decode batch against a weight) take Z = 4 or 2,
-// which needs K % 128 == 0 (k-atoms past K read as zero).
+// which needs whole k-tiles (k-atoms past K read as zero; see Stages).
 template <int BN, int AROWS, int Z>
 struct Tile {
     static_assert(AROWS == kBM || (AROWS <= 64 && AROWS % 8 == 0),
@@ -557,6 +557,23 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// K in stages of Z k-tiles.  A 3-D box brings Z whole k-tiles; the bytes behind
+// the last whole one (K % 128 != 0) are a stage of their own, one k-tile by 2-D
+// boxes, which read zeros past K.  (B200, against one k-tile to a stage and no
+// split: 40 x 1024 x 7184 21.4 -> 7.5 us, 64 x 16384 x 1040 11.0 -> 9.2.)
+template <int Z>
+struct Stages {
+    int ktiles, groups, all;  // k-tiles of the boxes, their stages, all stages
+    __device__ __forceinline__ explicit Stages(int K)
+        : ktiles(Z == 1 ? (K + kBK - 1) / kBK : K / kBK), groups((ktiles + Z - 1) / Z),
+          all(groups + (Z > 1 && K % kBK != 0 ? 1 : 0)) {}
+    __device__ __forceinline__ bool rest(int kg) const { return Z > 1 && kg == groups; }
+    // k-tiles of stage kg
+    __device__ __forceinline__ int of(int kg) const {
+        return rest(kg) ? 1 : ktiles - kg * Z < Z ? ktiles - kg * Z : Z;
+    }
+};
+
 // The loads of stage group kg (k-tiles kg*Z ...) of A rows m0.. and B rows
 // n0..: 2-D boxes for Z = 1, else one 3-D box of Z atoms per operand.
 template <int Z, int ABYTES, int BOFFSET>
@@ -580,6 +597,8 @@ template <int BN, int AROWS, int Z>
 __global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
     scaled_mm_kernel(const __grid_constant__ CUtensorMap tma_a,
                      const __grid_constant__ CUtensorMap tma_b,
+                     const __grid_constant__ CUtensorMap rest_a,
+                     const __grid_constant__ CUtensorMap rest_b,
                      const __grid_constant__ CUtensorMap tma_res,
                      const __grid_constant__ CUtensorMap tma_out, const GemmArgs g) {
     using T = Tile<BN, AROWS, Z>;
@@ -597,8 +616,7 @@ __global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles_n = (g.N + BN - 1) / BN;
     const int tiles = tiles_n * ((g.M + kBM - 1) / kBM);
-    const int ktiles = (g.K + kBK - 1) / kBK;
-    const int kgroups = (ktiles + Z - 1) / Z;
+    const Stages<Z> stages(g.K);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -637,7 +655,7 @@ __global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const int m0 = (t / tiles_n) * kBM, n0 = (t % tiles_n) * BN;
-                for (int kg = 0; kg < kgroups; ++kg, ++it) {
+                for (int kg = 0; kg < stages.all; ++kg, ++it) {
                     const int s = it % S;
                     // a fresh barrier counts as having completed the phase
                     // before phase 0: the first pass over the ring does not wait
@@ -645,9 +663,16 @@ __global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[s], T::kStageBytes);
-                    load_group<Z, T::kABytes, T::kBOffset>(smem + s * T::kStageBytes, &tma_a,
-                                                           &tma_b, &full[s], kg, m0, n0);
+                    uint8_t* dst = smem + s * T::kStageBytes;
+                    if (stages.rest(kg)) {
+                        mbar_arrive_expect_tx(&full[s], T::kABytes + T::kBBytes);
+                        tma_load_2d(dst, &rest_a, &full[s], stages.ktiles * kBK, m0);
+                        tma_load_2d(dst + T::kBOffset, &rest_b, &full[s], stages.ktiles * kBK, n0);
+                    } else {
+                        mbar_arrive_expect_tx(&full[s], T::kStageBytes);
+                        load_group<Z, T::kABytes, T::kBOffset>(dst, &tma_a, &tma_b, &full[s], kg,
+                                                               m0, n0);
+                    }
                 }
             }
             // the loads still in flight land before the CTA may exit
@@ -666,7 +691,7 @@ __global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
                 if (!wait_phase(&acc_empty[buf], ((j >> 1) & 1) ^ 1, g.err)) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem + (uint32_t)(buf * BN);
-                for (int kg = 0; kg < kgroups; ++kg, ++it) {
+                for (int kg = 0; kg < stages.all; ++kg, ++it) {
                     const int s = it % S;
                     if (!wait_phase(&full[s], (it / S) & 1, g.err)) {
                         ok = false;
@@ -674,8 +699,7 @@ __global__ void __launch_bounds__(Tile<BN, AROWS, Z>::kThreadsPerCta, 1)
                     }
                     tc_fence_after_sync();
                     const uint8_t* stage = smem + s * T::kStageBytes;
-                    // the k-tiles of the group that lie inside K
-                    const int nk = ktiles - kg * Z < Z ? ktiles - kg * Z : Z;
+                    const int nk = stages.of(kg);  // the k-tiles that lie inside K
                     for (int j = 0; j < nk; ++j) {
                         const uint64_t ad = kmajor_sw128_desc(stage + j * T::kABytes);
                         const uint64_t bd = kmajor_sw128_desc(stage + T::kBOffset + j * T::kBBytes);
@@ -1720,7 +1744,9 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
 template <int AROWS, bool MX>
 __global__ void __launch_bounds__(kThreads, 1)
     scaled_mm_split_kernel(const __grid_constant__ CUtensorMap tma_a,
-                           const __grid_constant__ CUtensorMap tma_b, const GemmArgs g,
+                           const __grid_constant__ CUtensorMap tma_b,
+                           const __grid_constant__ CUtensorMap rest_a,
+                           const __grid_constant__ CUtensorMap rest_b, const GemmArgs g,
                            const uint8_t* sfa, const uint8_t* sfb, int split) {
     using T = SplitTile<AROWS, MX>;
     constexpr int S = T::kStages, Z = T::Z, BN = T::kBN;
@@ -1738,9 +1764,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile = (int)blockIdx.x / split;
     const int tiles_n = (g.N + BN - 1) / BN;
     const int m0 = (tile / tiles_n) * kBM, n0 = (tile % tiles_n) * BN;
-    const int ktiles = g.K / kBK;  // K is a multiple of 128
-    const int kgroups = (ktiles + Z - 1) / Z;
-    const int k_lo = rank * kgroups / split, k_hi = (rank + 1) * kgroups / split;
+    const Stages<Z> stages(g.K);
+    const int ktiles = stages.ktiles;  // (MX: K is a multiple of 128)
+    const int k_lo = rank * stages.all / split, k_hi = (rank + 1) * stages.all / split;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -1770,7 +1796,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = it % S;
                 if (!wait_phase(&empty[s], ((it / S) & 1) ^ 1, g.err)) break;
                 uint8_t* dst = smem + s * T::kStageStride;
-                const int nk = ktiles - kg * Z < Z ? ktiles - kg * Z : Z;
+                if (!MX && stages.rest(kg)) {
+                    mbar_arrive_expect_tx(&full[s], T::kABytes + T::kBBytes);
+                    tma_load_2d(dst, &rest_a, &full[s], ktiles * kBK, m0);
+                    tma_load_2d(dst + T::kBOffset, &rest_b, &full[s], ktiles * kBK, n0);
+                    continue;
+                }
+                const int nk = stages.of(kg);
                 const uint32_t sf_bytes = MX ? (uint32_t)(nk * T::kSfBytes) : 0u;
                 mbar_arrive_expect_tx(&full[s], Z * (T::kABytes + T::kBBytes) + 2 * sf_bytes);
                 tma_load_3d(dst, &tma_a, &full[s], 0, m0, kg * Z);
@@ -1801,7 +1833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_phase(&full[s], (it / S) & 1, g.err)) break;
                 tc_fence_after_sync();
                 const uint8_t* stage = smem + s * T::kStageStride;
-                const int nk = ktiles - kg * Z < Z ? ktiles - kg * Z : Z;
+                const int nk = stages.of(kg);
                 for (int kj = 0; kj < nk; ++kj) {
                     if constexpr (MX) {
                         tmem_copy_32x128b_x4(tmem_sfa,
@@ -2313,6 +2345,16 @@ bool make_map3(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int 
            CUDA_SUCCESS;
 }
 
+// The 2-D maps of the operands' last bytes, where a kernel with several k-tiles
+// per stage needs them (else they are not read).
+bool make_rest_maps(CUtensorMap* ra, CUtensorMap* rb, const CUtensorMap& ma, const CUtensorMap& mb,
+                    const GemmArgs& g, const void* a, const void* b, int arows, int brows, int z) {
+    *ra = ma;
+    *rb = mb;
+    return z == 1 || g.K % kBK == 0 ||
+           (make_map(ra, a, g.M, g.K, arows) && make_map(rb, b, g.N, g.K, brows));
+}
+
 // The operand maps of a kernel that loads Z k-tiles per stage.
 bool make_maps(CUtensorMap* ma, CUtensorMap* mb, const GemmArgs& g, const void* a, const void* b,
                int arows, int brows, int z) {
@@ -2324,15 +2366,18 @@ template <int BN, int AROWS, int Z>
 cudaError_t launch_bn(const GemmArgs& g, const void* a, const void* b, int sm_count,
                       cudaStream_t stream) {
     using T = Tile<BN, AROWS, Z>;
-    CUtensorMap ma, mb, mr, mo;
-    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z) || !make_epilogue_maps(&mr, &mo, g, T::kChunk))
+    CUtensorMap ma, mb, ra, rb, mr, mo;
+    if (!make_maps(&ma, &mb, g, a, b, AROWS, BN, Z) ||
+        !make_rest_maps(&ra, &rb, ma, mb, g, a, b, AROWS, BN, Z) ||
+        !make_epilogue_maps(&mr, &mo, g, T::kChunk))
         return cudaErrorInvalidValue;
     constexpr auto kernel = scaled_mm_kernel<BN, AROWS, Z>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((g.N + BN - 1) / BN) * ((g.M + kBM - 1) / kBM);
     const unsigned grid = (unsigned)(tiles < sm_count ? tiles : sm_count);  // one CTA per SM
-    return launch_persistent(kernel, grid, T::kThreadsPerCta, T::kSmemBytes, stream, ma, mb, mr, mo, g);
+    return launch_persistent(kernel, grid, T::kThreadsPerCta, T::kSmemBytes, stream, ma, mb, ra,
+                             rb, mr, mo, g);
 }
 
 // sfa, sfb: the MX form's scale codes of a and b (the blocked order), else
@@ -2389,8 +2434,9 @@ template <int AROWS, bool MX>
 cudaError_t launch_split(const GemmArgs& g, const void* a, const void* b, const uint8_t* sfa,
                          const uint8_t* sfb, int64_t tiles, int split, cudaStream_t stream) {
     using T = SplitTile<AROWS, MX>;
-    CUtensorMap ma, mb;
-    if (!make_map3(&ma, a, g.M, g.K, AROWS, T::Z) || !make_map3(&mb, b, g.N, g.K, T::kBN, T::Z))
+    CUtensorMap ma, mb, ra, rb;
+    if (!make_map3(&ma, a, g.M, g.K, AROWS, T::Z) || !make_map3(&mb, b, g.N, g.K, T::kBN, T::Z) ||
+        !make_rest_maps(&ra, &rb, ma, mb, g, a, b, AROWS, T::kBN, T::Z))
         return cudaErrorInvalidValue;
     constexpr auto kernel = scaled_mm_split_kernel<AROWS, MX>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
@@ -2409,7 +2455,7 @@ cudaError_t launch_split(const GemmArgs& g, const void* a, const void* b, const 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, g, sfa, sfb, split);
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, ra, rb, g, sfa, sfb, split);
 }
 
 template <bool MX>
@@ -2498,8 +2544,8 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
 // in rounds.  The first takes e + k-tiles * c, a further one e2 + k-tiles * c2
 // but at least what a tile's epilogue takes, which the products of the next
 // tile only hide.  Measured on B200 (us above the 3.7 of an empty call; N =
-// 256 .. 65536, M = 1 .. 4096, K = 128 .. 7168, silu and residual; K % 128 !=
-// 0: c 0.35 for 64 columns):
+// 256 .. 65536, M = 1 .. 4096, K = 128 .. 7168, silu and residual; K <
+// 128: c 0.35 for 64 columns):
 //                                      e    c        further rounds
 //   swapped, at most  8 rows           0    0.085    0.95 + 0.085 k
 //                    16 rows           0    0.113    1.6 + 0.113 k
@@ -2530,7 +2576,8 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
 // columns) for 18.1 and 36.2 (pairs).
 GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) {
     GemmPlan best;
-    const bool atoms = K % kBK == 0;  // several k-tiles per box
+    const bool whole = K % kBK == 0;  // (the swapped kernel takes no other K)
+    const bool boxes = K >= kBK;      // several k-tiles per box
     const int64_t ktiles = (K + kBK - 1) / kBK;
     double lowest = -1.0;
     auto offer = [&](const GemmPlan& p, double e, double cost) {
@@ -2559,7 +2606,7 @@ GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_cou
               r.e + k * r.c +
                   (double)((p.tiles - 1) / units) * (further > r.least ? further : r.least));
     };
-    if (M <= 32 && atoms) {
+    if (M <= 32 && whole) {
         const int rows = M <= 8 ? 8 : M <= 16 ? 16 : 32;
         const double c = rows == 8    ? (mx ? 0.15 : 0.085)
                          : rows == 16 ? (mx ? 0.15 : 0.113)
@@ -2571,29 +2618,30 @@ GemmPlan plan_scaled_mm_act(int64_t M, int64_t N, int64_t K, bool mx, int sm_cou
                     c, 0.0});
     }
     if (M <= 64) {
-        offer_tile(kGemmTile, 64, 64, atoms ? 4 : 1,
-                   atoms ? Rounds{0.4, mx ? 0.255 : 0.195, 1.2, mx ? 0.255 : 0.235, 2.0}
+        offer_tile(kGemmTile, 64, 64, boxes ? 4 : 1,
+                   boxes ? Rounds{0.4, mx ? 0.255 : 0.195, 1.2, mx ? 0.255 : 0.235, 2.0}
                          : Rounds{0.4, 0.35, 0.4, 0.35, 2.0});
-        if (atoms) offer_tile(kGemmTile, 64, 128, 2, {1.1, mx ? 0.31 : 0.245, 1.5, 0.36, 2.6});
+        if (boxes) offer_tile(kGemmTile, 64, 128, 2, {1.1, mx ? 0.31 : 0.245, 1.5, 0.36, 2.6});
     } else {
-        const double c = !atoms ? 0.35 : mx ? 0.31 : 0.245;
-        offer_tile(kGemmTile, kBM, 64, atoms ? 2 : 1, {0.4, c, 0.7, c, 2.3});
+        const double c = !boxes ? 0.35 : mx ? 0.31 : 0.245;
+        offer_tile(kGemmTile, kBM, 64, boxes ? 2 : 1, {0.4, c, 0.7, c, 2.3});
     }
-    if (M > 64 || !atoms) {
+    if (M > 64 || !boxes) {
         offer_tile(kGemmTile, kBM, 128, 1,
                    mx ? Rounds{1.2, 0.37, 1.1, 0.37, 3.1} : Rounds{1.2, 0.31, 1.5, 0.33, 3.1});
     }
     if (M > 128)
         offer_tile(kGemmPair, 256, 256, 1,
                    mx ? Rounds{4.0, 0.44, 5.6, 0.43, 0.0} : Rounds{4.3, 0.35, 3.5, 0.45, 4.9});
-    if (atoms) {
+    if (boxes) {
         GemmPlan p;
         p.kernel = kGemmSplit;
         p.a_rows = M <= 32 ? 32 : M <= 64 ? 64 : kBM;
         p.tile_n = 64;
         p.k_tiles_per_stage = M <= 64 ? 4 : 2;
         p.tiles = ((M + kBM - 1) / kBM) * ((N + 63) / 64);
-        const int64_t groups = (ktiles + p.k_tiles_per_stage - 1) / p.k_tiles_per_stage;
+        const int64_t groups = (K / kBK + p.k_tiles_per_stage - 1) / p.k_tiles_per_stage +
+                               (whole ? 0 : 1);  // (the last bytes are a stage)
         const double e = M <= 32 ? 0.0 : M <= 64 ? 0.3 : 1.7;
         const double c = M <= 32 ? 0.21 : M <= 64 ? 0.225 : 0.25;
         const int64_t resident[3] = {sm_count / 2, (int64_t)32 * sm_count / 148,

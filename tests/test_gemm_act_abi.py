@@ -66,7 +66,9 @@ def test_cpu_tensors_and_unknown_activations_are_refused(rrf):
     (128, 2048, 7168, False, ("split", 128, 64, 2, 32, 128)),
     (1999, 2576, 1024, True, ("tile", 128, 128, 1, 336, 148)),
     (64, 1024, 7168, True, ("split", 64, 64, 4, 16, 64)),
-    (40, 4096, 1040, False, ("tile", 64, 64, 1, 64, 64))])  # K % 128 != 0
+    (40, 4096, 1040, False, ("split", 64, 64, 4, 64, 128)),  # K % 128 != 0
+    (8, 1024, 4112, False, ("split", 32, 64, 4, 16, 64)),
+    (40, 4096, 112, False, ("tile", 64, 64, 1, 64, 64))])
 def test_plan(rrf, m, n, k, mx, want):
     p = rrf.rrf_plan_scaled_mm_act(m, n, k, 148, mx=mx)
     assert (p["kernel"], p["a_rows"], p["tile_n"], p["k_tiles_per_stage"], p["tiles"],
@@ -90,13 +92,14 @@ def test_plan_invariants(rrf, sms):
                         split, left = divmod(p["ctas"], p["tiles"])
                         assert split in (2, 4, 8) and left == 0 and p["ctas"] <= sms
                         # every CTA has a part of K
-                        assert k % 128 == 0 and -(-k // 128 // p["k_tiles_per_stage"]) >= split
+                        z = p["k_tiles_per_stage"]
+                        assert k >= 128 and -(-(k // 128) // z) + (k % 128 != 0) >= split
                         assert rows >= min(m, 128)
                     else:
                         assert p["ctas"] == min(p["tiles"], sms // 2) * 2 if kernel == "pair" \
                             else p["ctas"] == min(p["tiles"], sms)
                     if kernel == "tile":
-                        assert (rows == 64) == (m <= 64 and not (columns == 128 and k % 128))
+                        assert (rows == 64) == (m <= 64 and not (columns == 128 and k < 128))
 
 
 def test_plan_refusals(rrf):

@@ -109,7 +109,14 @@ FP8 = [(1, 256, 128, "swap", 8, 64), (9, 528, 640, "swap", 16, 64),
        (1, 2000, 4224, "split", 32, 4), (8, 912, 4224, "split", 32, 8),
        (64, 4624, 1664, "split", 64, 2), (40, 1040, 3200, "split", 64, 4),
        (33, 272, 7168, "split", 64, 8), (100, 4624, 2048, "split", 128, 2),
-       (250, 784, 3456, "split", 128, 4), (129, 336, 4352, "split", 128, 8)]
+       (250, 784, 3456, "split", 128, 4), (129, 336, 4352, "split", 128, 8),
+       # K % 128 != 0 behind boxes of several k-tiles
+       (64, 5120, 528, "tile", 64, 64), (37, 272, 272, "tile", 64, 64),
+       (3, 7184, 1040, "tile", 64, 64), (50, 16400, 1136, "tile", 64, 128),
+       (200, 272, 400, "tile", 128, 64), (100, 4112, 656, "tile", 128, 64),
+       (24, 336, 1552, "split", 32, 4), (40, 1040, 3216, "split", 64, 4),
+       (8, 912, 4240, "split", 32, 8), (129, 336, 4368, "split", 128, 8),
+       (100, 4624, 2064, "split", 128, 2)]
 MX = [(1, 256, 128, "swap", 8, 64), (16, 208, 512, "swap", 16, 64),
       (29, 7168, 1664, "swap", 32, 64), (60, 1040, 384, "tile", 64, 64),
       (33, 16400, 640, "tile", 64, 128), (200, 272, 384, "tile", 128, 64),
