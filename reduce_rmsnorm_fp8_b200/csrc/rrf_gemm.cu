@@ -234,6 +234,15 @@ __host__ __device__ constexpr uint32_t f8_idesc(int bn) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// (y * a) * b, both products rounded.  The second is two scalar products: a
+// packed one whose result goes into a packed sum is compiled into one fused
+// multiply-add (also where both are written as .rn; measured), which would
+// leave a rounding of out = (sum * a_scale) * b_scale + bias out.
+__device__ __forceinline__ float2 scaled(float2 y, float2 a, float2 b) {
+    const float2 z = __fmul2_rn(y, a);
+    return make_float2(__fmul_rn(z.x, b.x), __fmul_rn(z.y, b.y));
+}
+
 // (2^t) and (1 / t) of both halves; results below 2^-126 are 0.
 __device__ __forceinline__ float2 exp2_pair(float2 t) {
     float2 r;
@@ -431,8 +440,7 @@ struct EpiWarp {
             for (int i = 0; i < 8; ++i) {
                 const float4 s = columns[8 * h + i];
                 y[i] = make_float2(v[2 * i], v[2 * i + 1]);
-                if constexpr (SCALED)
-                    y[i] = __fmul2_rn(__fmul2_rn(y[i], both(sa)), make_float2(s.x, s.y));
+                if constexpr (SCALED) y[i] = scaled(y[i], both(sa), make_float2(s.x, s.y));
                 y[i] = __fadd2_rn(y[i], make_float2(s.z, s.w));
             }
             activate_all<8>(g.act, y);
@@ -1174,7 +1182,7 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
                             const float2 sa =
                                 make_float2(2 * m < g.M ? __ldg(g.a_scale + 2 * m) : 0.0f,
                                             2 * m + 1 < g.M ? __ldg(g.a_scale + 2 * m + 1) : 0.0f);
-                            y[m] = __fmul2_rn(__fmul2_rn(y[m], sa), both(sb));
+                            y[m] = scaled(y[m], sa, both(sb));
                         }
                         if (g.bias != nullptr) y[m] = __fadd2_rn(y[m], both(bias));
                     }
@@ -1917,8 +1925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 4; ++q) {
             const int col = n + 2 * q;
             if constexpr (!MX)
-                y[q] = __fmul2_rn(__fmul2_rn(y[q], both(sa)),
-                                  make_float2(g.b_scale[col], g.b_scale[col + 1]));
+                y[q] = scaled(y[q], both(sa), make_float2(g.b_scale[col], g.b_scale[col + 1]));
             if (g.bias != nullptr)
                 y[q] = __fadd2_rn(y[q], make_float2(__uint_as_float((uint32_t)g.bias[col] << 16),
                                                     __uint_as_float((uint32_t)g.bias[col + 1] << 16)));

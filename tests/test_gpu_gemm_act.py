@@ -310,3 +310,30 @@ def test_wait_timeout_is_reported(rrf, m, n, k, mx):
     out = call(rrf, p, "silu")
     check(p, out, "silu", p["residual"])
     assert torch.equal(out, call(rrf, p, "silu"))
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 4096, 128), (14, 2048, 256), (30, 2048, 128), (40, 2048, 384),
+                                   (40, 2048, 144), (200, 1024, 256), (1000, 2576, 128),
+                                   (3000, 2576, 256), (1, 1024, 4224), (64, 1024, 4096),
+                                   (250, 784, 3456)])
+def test_scales_and_bias_round_one_by_one(rrf, m, n, k):
+    """((sum * a_scale) * b_scale) + bias, each step rounded to fp32: bit for
+    bit, in the plain product and in the one with an epilogue.  The sums are
+    small integers (exact in fp32 in any order), and the bias takes most of the
+    first row away, so that a step left unrounded shows in one value of some
+    hundred."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + n)
+    a, b = (torch.randint(-2, 4, (rows, k), generator=g, device="cuda").float().to(
+        torch.float8_e4m3fn) for rows in (m, n))
+    sums = (a.double() @ b.double().T).float()
+    sa = 0.5 + torch.rand(m, generator=g, device="cuda") / 64
+    sb = 0.5 + torch.rand(n, generator=g, device="cuda")
+    y = (sums * sa[:, None]) * sb
+    bias = -y[0].bfloat16()
+    want = (y + bias.float()).bfloat16()
+    assert torch.equal(rrf.rrf_scaled_mm_fp8(a, sa, b, sb, bias), want)
+    assert torch.equal(rrf.rrf_scaled_mm_fp8_act(a, sa, b, sb, bias), want)
+    # (the case can tell: with one rounding fewer some values differ)
+    once = (sums.double() * sa.double()[:, None]).float().double() * sb.double() + bias.double()
+    assert bool((once.float().bfloat16() != want).any())
