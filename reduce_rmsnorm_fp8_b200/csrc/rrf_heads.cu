@@ -89,7 +89,8 @@ __device__ __forceinline__ float fast_reciprocal(float v) {
 // which makes a representable quotient exact and any other one correct to
 // about half an ulp.  Rows above 1e30 are scaled by 2^-64 first, so that n
 // stays finite.  Values beyond a bound (scale_ub) saturate; only where they are
-// 1e30 times the bound, and y might not be finite, is it left uncorrected.
+// 1e30 times the bound or infinite, and y might not be finite, is the row left
+// uncorrected (an infinite y would make its remainder a NaN).
 // (Cutting x to the bound instead costs every row some 20 instructions.)
 __device__ __forceinline__ float quantise(const float2 x[8], float most, float scale_ub, uint2& qa,
                                           uint2& qb) {
@@ -100,8 +101,9 @@ __device__ __forceinline__ float quantise(const float2 x[8], float most, float s
     float2 y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(x[i], k2);
-    // (an infinite scale: finite values are 0, infinities NaN)
-    if (most <= m * 1e30f && d < __int_as_float(0x7F800000)) {
+    // (an infinite scale: finite values are 0, infinities NaN.  For m above
+    // 3.4e8 m * 1e30 is infinite, and y at most 448 * 3.4e38 / m.)
+    if (most <= m * 1e30f && most < __int_as_float(0x7F800000)) {
         const float2 minus_d = make_float2(-d, -d), f2 = make_float2(f, f);
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll

@@ -241,6 +241,25 @@ def test_special_rows_of_the_cache(rrf, scale_ub, dim):
             assert bool(((v[i] - y).abs()[ok] <= (step / 2 + 4 * ref.U * y.abs())[ok]).all()), name
 
 
+@pytest.mark.parametrize("scale_ub", [2.0 ** e for e in (28, 29, 30, 66, 100, 127)])
+@pytest.mark.parametrize("dim", [64, 80])
+def test_special_rows_under_a_large_bound(rrf, scale_ub, dim):
+    """A finite bound cuts an infinity however large it is: 448 times it, as a
+    quotient, may pass fp32.  (Powers of two: the bound itself is not rounded.)"""
+    test_special_rows_of_the_cache(rrf, scale_ub, dim)
+    # the values of the one pass go by the same rule
+    x = torch.stack([f(dim) for f in SPECIAL.values()]).bfloat16()[:, None].cuda()
+    n = x.shape[0]
+    one, two = new_cache(gen(1), n, 1, 1, dim), new_cache(gen(1), n, 1, 1, dim)
+    slots, gamma = torch.arange(n, device="cuda"), torch.ones(dim, device="cuda").bfloat16()
+    y = torch.ones_like(x)
+    rrf.rrf_kv_cache_write_fp8(y, x, slots, *one, scale_ub=scale_ub)
+    rrf.rrf_qk_norm_rope_kv_cache_fp8(y, y, x, gamma, gamma, 0.0, 0.0, None, None, slots, *two,
+                                      scale_ub=scale_ub)
+    assert torch.equal(one[2].view(torch.uint8), two[2].view(torch.uint8))
+    assert torch.equal(one[3], two[3])
+
+
 def test_special_rows_of_the_norm(rrf):
     dim = 64
     q, k, _, qg, kg, table, pos = problem(12, 4, 2, 1, dim, 64)
