@@ -1715,7 +1715,9 @@ __global__ void __launch_bounds__(MxTile<BN, AROWS, Z>::kThreadsPerCta, 1)
 // every row of its partial sums to the CTA of the cluster that finishes the
 // row (row r: CTA r / (AROWS / S)), which adds the S parts in the order of
 // their ranks and runs the epilogue on its rows.  The parts travel through
-// distributed shared memory: no workspace, and the same bits every time.
+// distributed shared memory: no workspace, and the same bits every time.  A CTA
+// whose part did not come (a wait ran out) tells the cluster, which then stores
+// nothing.
 // B200: 64 x 1024 x 7168 in 7.2 us by 4 CTAs to a tile (15.6 us by one).
 template <int AROWS, bool MX>
 struct SplitTile {
@@ -1749,6 +1751,12 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
                  : "memory");
 }
 
+// Set `flag` in every CTA of the cluster.
+__device__ __forceinline__ void set_in_cluster(uint32_t* flag, int ctas) {
+    for (int r = 0; r < ctas; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], 1;" :: "r"(peer_smem(flag, (uint32_t)r)) : "memory");
+}
+
 template <int AROWS, bool MX>
 __global__ void __launch_bounds__(kThreads, 1)
     scaled_mm_split_kernel(const __grid_constant__ CUtensorMap tma_a,
@@ -1766,6 +1774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    uint32_t* failed = tmem_slot + 1;  // a part of the tile's sums is missing
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
@@ -1782,6 +1791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
+        *failed = 0;
         fence_mbar_init_cluster();
     }
     if (warp == 1) {
@@ -1838,7 +1848,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0;
             for (int kg = k_lo; kg < k_hi; ++kg, ++it) {
                 const int s = it % S;
-                if (!wait_phase(&full[s], (it / S) & 1, g.err)) break;
+                if (!wait_phase(&full[s], (it / S) & 1, g.err)) {
+                    set_in_cluster(failed, split);
+                    break;
+                }
                 tc_fence_after_sync();
                 const uint8_t* stage = smem + s * T::kStageStride;
                 const int nk = stages.of(kg);
@@ -1872,6 +1885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = quarter * 32 + lane, own = AROWS / split;
         bool have = epilogue_wait(acc_full, 0, g);
         have = __all_sync(0xFFFFFFFFu, have);
+        if (!have && lane == 0) set_in_cluster(failed, split);
         tc_fence_after_sync();
         if (quarter * 32 < AROWS && m0 + quarter * 32 < g.M && have) {
             const uint32_t to = peer_smem(
@@ -1897,7 +1911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         tmem_dealloc(tmem, T::kTmemCols);
     }
-    if (warp < 2) return;
+    if (warp < 2 || *failed != 0) return;
 
     // ---- the epilogue of this CTA's rows, 8 columns to a thread
     const int own = AROWS / split;

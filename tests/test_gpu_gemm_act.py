@@ -337,3 +337,24 @@ def test_scales_and_bias_round_one_by_one(rrf, m, n, k):
     # (the case can tell: with one rounding fewer some values differ)
     once = (sums.double() * sa.double()[:, None]).float().double() * sb.double() + bias.double()
     assert bool((once.float().bfloat16() != want).any())
+
+
+@pytest.mark.parametrize("m,n,k,kernel,mx", [
+    (4, 1024, 4096, "split", False), (60, 1024, 4096, "split", True),
+    (64, 4624, 1664, "split", False), (129, 336, 4352, "split", False),
+    (100, 4624, 2048, "split", True), (4, 7168, 512, "swap", False), (4, 7168, 512, "swap", True),
+    (64, 5120, 528, "tile", False), (200, 7168, 1024, "tile", False),
+    (200, 7168, 1024, "tile", True), (500, 7168, 2048, "pair", False),
+    (500, 7168, 2048, "pair", True)])
+def test_a_wait_that_ran_out_stores_nothing(rrf, m, n, k, kernel, mx):
+    """An output tile whose sums did not come is left as it was."""
+    assert rrf.rrf_plan_scaled_mm_act(m, n, k, SMS, mx=mx)["kernel"] == kernel
+    p = problem(rrf, 6, m, n, k, mx)
+    out = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    rrf.rrf_debug_starve_next_gemm()
+    call(rrf, p, "silu", out=out)
+    torch.cuda.synchronize()
+    assert rrf.rrf_device_error(clear=True) & rrf.RRF_DEVICE_ERROR_GEMM_TIMEOUT
+    assert bool((out == 7).all())
+    check(p, call(rrf, p, "silu", out=out), "silu", p["residual"])
