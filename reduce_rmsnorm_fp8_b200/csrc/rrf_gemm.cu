@@ -904,8 +904,12 @@ __device__ __forceinline__ uint4 ld_residual(const uint4* p) {
 }
 
 // sfx, sfw: the MX form's scale codes of the call's rows and of the weight
-// (the blocked order); null in the per-token form.
-template <int NA, int Z, bool MX>
+// (the blocked order); null in the per-token form.  EPI: the form with
+// activation and residual.  The plain product has its own, because the code of
+// the activations and the residual's registers cost a short call up to a tenth
+// (B200, 4096 x 512: 8 rows 3.5 us in one form for both, 3.35 apart; 32 rows
+// 4.75 and 4.05, MX 4.9 and 4.45).
+template <int NA, int Z, bool MX, bool EPI>
 __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
     scaled_mm_swap_pairk_kernel(const __grid_constant__ CUtensorMap tma_x,
                                 const __grid_constant__ CUtensorMap tma_w, const GemmArgs g,
@@ -1144,7 +1148,7 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
             if (!odd && n < g.N) {
                 if constexpr (!MX) sb = g.b_scale[n];
                 if (g.bias != nullptr) bias = __uint_as_float((uint32_t)g.bias[n] << 16);
-                if (g.residual != nullptr) {
+                if (EPI && g.residual != nullptr) {
 #pragma unroll
                     for (int m = 0; m < NA; ++m)
                         if (m < g.M) res[m] = ld_residual(g.residual + (int64_t)m * g.N + n);
@@ -1186,12 +1190,12 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
                         }
                         if (g.bias != nullptr) y[m] = __fadd2_rn(y[m], both(bias));
                     }
-                    activate_all<NA / 2>(g.act, y);
+                    if constexpr (EPI) activate_all<NA / 2>(g.act, y);
 #pragma unroll
                     for (int m = 0; m < NA; ++m) {
                         if (m < g.M) {
                             float z = m % 2 ? y[m / 2].y : y[m / 2].x;
-                            if (g.residual != nullptr)
+                            if (EPI && g.residual != nullptr)
                                 z = __fadd_rn(z, __uint_as_float((uint32_t)res[m] << 16));
                             g.out[(int64_t)m * g.N + n] =
                                 (uint16_t)(f32x2_to_bf16x2(z, 0.0f) & 0xFFFFu);
@@ -2403,21 +2407,29 @@ cudaError_t launch_bn(const GemmArgs& g, const void* a, const void* b, int sm_co
 
 // sfa, sfb: the MX form's scale codes of a and b (the blocked order), else
 // null.
-template <int NA, int Z, bool MX = false>
-cudaError_t launch_swap_pairk(const GemmArgs& g, const void* a, const void* b, int sm_count,
-                              cudaStream_t stream, const uint8_t* sfa = nullptr,
-                              const uint8_t* sfb = nullptr) {
+template <int NA, int Z, bool MX, bool EPI>
+cudaError_t launch_swap_form(const GemmArgs& g, const void* a, const void* b, int sm_count,
+                             cudaStream_t stream, const uint8_t* sfa, const uint8_t* sfb) {
     using T = SwapPairTile<NA, Z, MX>;
     CUtensorMap mx, mw;
     if (!make_map3(&mx, a, g.M, g.K, NA, Z) || !make_map3(&mw, b, g.N, g.K, T::kWRows, Z))
         return cudaErrorInvalidValue;
-    constexpr auto kernel = scaled_mm_swap_pairk_kernel<NA, Z, MX>;
+    constexpr auto kernel = scaled_mm_swap_pairk_kernel<NA, Z, MX, EPI>;
     const cudaError_t e = enable_dynamic_smem<kernel>(T::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (g.N + T::kWRows - 1) / T::kWRows;
     const unsigned grid = (unsigned)(tiles < sm_count ? tiles : sm_count);
     return launch_persistent(kernel, grid, T::kThreadsPerCta, T::kSmemBytes, stream, mx, mw, g, sfa,
                              sfb);
+}
+
+template <int NA, int Z, bool MX = false>
+cudaError_t launch_swap_pairk(const GemmArgs& g, const void* a, const void* b, int sm_count,
+                              cudaStream_t stream, const uint8_t* sfa = nullptr,
+                              const uint8_t* sfb = nullptr) {
+    return g.act == kPlainProduct
+               ? launch_swap_form<NA, Z, MX, false>(g, a, b, sm_count, stream, sfa, sfb)
+               : launch_swap_form<NA, Z, MX, true>(g, a, b, sm_count, stream, sfa, sfb);
 }
 
 cudaError_t launch_pair(const GemmArgs& g, const void* a, const void* b, int sm_count,
