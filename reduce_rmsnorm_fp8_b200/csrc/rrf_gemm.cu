@@ -411,9 +411,9 @@ struct EpiWarp {
                                           int row_next, int n_next, AfterRead after_read) {
         uint4* box = reinterpret_cast<uint4*>(boxes + (count % BOXES) * kBoxBytes);
         if (loading) {
-            loading = false;
             const bool ok = wait_phase(&bars[count % BOXES], (count / BOXES) & 1, g.err);
-            if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+            if (!__all_sync(0xFFFFFFFFu, ok)) return false;  // (finish() waits once more)
+            loading = false;
         }
         if (!inside(row0, n)) {  // uniform in the warp
             after_read();
