@@ -319,9 +319,10 @@ __device__ __forceinline__ void activate_all(int act, float2 y[PAIRS]) {
 // The epilogue of a warp's 32 rows (one accumulator lane each) and a quarter of
 // the tile's columns (a chunk: 64, 32 or 16).  A lane holds a row, but memory is
 // read and written in boxes of 32 rows x a chunk: a TMA load brings the
-// residual's box into shared memory a chunk ahead, each lane adds its row to it
-// in place, and a TMA store takes the box out (rows and columns past the matrix
-// are not written).  Boxes are swizzled over their rows' 128, 64 or 32 bytes
+// residual into the warp's box, each lane adds its row to it in place, and a TMA
+// store takes the box out (rows and columns past the matrix are not written).
+// The next chunk's residual is loaded once that store has read the box, so it
+// travels while the warp waits for the next tile's sums.  Boxes are swizzled over their rows' 128, 64 or 32 bytes
 // (16-byte piece p of row r at p ^ r % 8, p ^ r / 2 % 4 or p ^ r / 4 % 2), so
 // that a column of rows does not meet in a bank.  The scales and the bias of the
 // chunk's columns are loaded a chunk ahead too.
@@ -337,15 +338,15 @@ __device__ __forceinline__ void activate_all(int act, float2 y[PAIRS]) {
 // x 1024 6.8 -> 6.1.
 constexpr int kPairChunk = 64;  // columns of a chunk, on SM pairs
 
-// Of `warps` epilogue warps with `boxes` boxes each: the boxes (1024-byte
-// aligned), per warp a (scale, scale, bias, bias) for each pair of columns,
-// and per box a barrier.
-template <int WARPS, int BOXES, int CHUNK>
+// Of WARPS epilogue warps: a box each (1024-byte aligned, or as many bytes as
+// it has), a (scale, scale, bias, bias) for each pair of its columns, and the
+// box's barrier.
+template <int WARPS, int CHUNK>
 struct EpiLayout {
     static constexpr int kBoxBytes = 32 * CHUNK * 2;
-    static constexpr int kColumns = WARPS * BOXES * kBoxBytes;
+    static constexpr int kColumns = WARPS * kBoxBytes;
     static constexpr int kBarriers = kColumns + WARPS * CHUNK * 8;
-    static constexpr int kBytes = kBarriers + WARPS * BOXES * 8;
+    static constexpr int kBytes = kBarriers + WARPS * 8;
 };
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x,
@@ -363,31 +364,31 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // One epilogue warp: chunk() works on the chunks of its tiles in turn.
-template <int WARPS, int BOXES, bool SCALED, int CHUNK>
+template <int WARPS, bool SCALED, int CHUNK>
 struct EpiWarp {
-    using L = EpiLayout<WARPS, BOXES, CHUNK>;
+    using L = EpiLayout<WARPS, CHUNK>;
     static constexpr int kBoxBytes = L::kBoxBytes;
     static constexpr int kPieces = CHUNK / 8;  // 16-byte pieces of a box's row
     const GemmArgs& g;
     const CUtensorMap* res_map;
     const CUtensorMap* out_map;
-    uint8_t* boxes;
+    uint4* box;
     float4* columns;
-    uint64_t* bars;
+    uint64_t* bar;
     int lane;
-    int count;           // chunks inside the matrix so far; chunk k has box k % BOXES
-    bool loading;        // the next chunk's residual box is on its way
+    uint32_t phase;      // that the next load of the box completes
+    bool loading;        // the next chunk's residual is on its way into the box
     float2 scale, bias;  // of the next chunk's columns 2 lane, 2 lane + 1
 
     __device__ __forceinline__ EpiWarp(const GemmArgs& args, const CUtensorMap* rm,
                                        const CUtensorMap* om, uint8_t* area, int warp, int l)
-        : g(args), res_map(rm), out_map(om), boxes(area + warp * BOXES * kBoxBytes),
+        : g(args), res_map(rm), out_map(om),
+          box(reinterpret_cast<uint4*>(area + warp * kBoxBytes)),
           columns(reinterpret_cast<float4*>(area + L::kColumns + warp * CHUNK * 8)),
-          bars(reinterpret_cast<uint64_t*>(area + L::kBarriers) + warp * BOXES), lane(l),
-          count(0), loading(false), scale(both(1.0f)), bias(both(-0.0f)) {}
+          bar(reinterpret_cast<uint64_t*>(area + L::kBarriers) + warp), lane(l), phase(0), loading(false), scale(both(1.0f)), bias(both(-0.0f)) {}
 
     static __device__ __forceinline__ void init_barriers(uint8_t* area) {
-        for (int i = 0; i < WARPS * BOXES; ++i)
+        for (int i = 0; i < WARPS; ++i)
             mbar_init(reinterpret_cast<uint64_t*>(area + L::kBarriers) + i, 1);
     }
 
@@ -397,8 +398,8 @@ struct EpiWarp {
         load_box(row0, n);
     }
 
-    // Lane 0: no store reads a box any more.
-    __device__ __forceinline__ void boxes_free() const {
+    // Lane 0: no store reads the box any more.
+    __device__ __forceinline__ void box_free() const {
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
 
@@ -409,22 +410,21 @@ struct EpiWarp {
     template <class AfterRead>
     __device__ __forceinline__ bool chunk(uint32_t taddr, float sa, int row0, int n, bool more,
                                           int row_next, int n_next, AfterRead after_read) {
-        uint4* box = reinterpret_cast<uint4*>(boxes + (count % BOXES) * kBoxBytes);
         if (loading) {
-            const bool ok = wait_phase(&bars[count % BOXES], (count / BOXES) & 1, g.err);
+            const bool ok = wait_phase(bar, phase, g.err);
             if (!__all_sync(0xFFFFFFFFu, ok)) return false;  // (finish() waits once more)
             loading = false;
+            phase ^= 1;
         }
         if (!inside(row0, n)) {  // uniform in the warp
             after_read();
             if (more) {
-                boxes_free();
+                box_free();
                 ahead(row_next, n_next);
             }
             __syncwarp();
             return true;
         }
-        ++count;
         if (lane < CHUNK / 2) columns[lane] = make_float4(scale.x, scale.y, bias.x, bias.y);
         __syncwarp();
         if (more) load_columns(n_next);
@@ -457,28 +457,21 @@ struct EpiWarp {
             }
             lo = f32x2_to_bf16x8(y);
             hi = f32x2_to_bf16x8(y + 4);
-            if (h == 1 && BOXES > 1) {
-                // the other box's store began a chunk ago
-                boxes_free();
-                if (more) load_box(row_next, n_next);
-            }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tma_store_2d(out_map, box, n, row0);
-        if (BOXES == 1) {
-            boxes_free();
-            if (more) load_box(row_next, n_next);
-        }
+        box_free();
+        if (more) load_box(row_next, n_next);
         __syncwarp();
         return true;
     }
 
-    // Before the block's end: its stores have read their boxes, and (after a
+    // Before the block's end: its stores have read their box, and (after a
     // wait that ran out) the residual on its way has landed.
     __device__ __forceinline__ void finish() {
-        if (loading) wait_phase(&bars[count % BOXES], (count / BOXES) & 1, g.err);
-        boxes_free();
+        if (loading) wait_phase(bar, phase, g.err);
+        box_free();
     }
 
   private:
@@ -490,9 +483,8 @@ struct EpiWarp {
         if (g.residual == nullptr || !inside(row0, n)) return;
         loading = true;
         if (lane == 0) {
-            uint64_t* bar = &bars[count % BOXES];
             mbar_arrive_expect_tx(bar, kBoxBytes);
-            tma_load_2d(boxes + (count % BOXES) * kBoxBytes, res_map, bar, n, row0);
+            tma_load_2d(box, res_map, bar, n, row0);
         }
     }
 
@@ -538,7 +530,7 @@ struct Tile {
     // with 64-row A stages only the first two quarters of the accumulator
     // hold rows, and only their warps have boxes
     static constexpr int kEpiAreas = AROWS == kBM ? kEpiWarps : kEpiWarps / 2;
-    using Epi = EpiWarp<kEpiAreas, 1, true, kChunk>;
+    using Epi = EpiWarp<kEpiAreas, true, kChunk>;
     // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 8
     // at 64 (one k-tile), 4 with two k-tiles, 3 with four of 64 rows
     static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
@@ -1311,7 +1303,6 @@ __device__ __forceinline__ void grouped_tile(int t, int tiles_m, int tiles_n, in
 // 64 columns.
 constexpr int kPairEpiWarps = 16;
 constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
-constexpr int kPairBoxes = 1;
 constexpr int kPairStages = 4;
 
 struct PairTile {
@@ -1320,7 +1311,7 @@ struct PairTile {
     static constexpr int kStages = kPairStages;             // 128 KB
     static constexpr int kTmemCols = 512;                   // two 256-column accumulators
     static constexpr int kBarriers = 2 * kStages + 4 + 1;
-    using Epi = EpiWarp<kPairEpiWarps, kPairBoxes, true, kPairChunk>;
+    using Epi = EpiWarp<kPairEpiWarps, true, kPairChunk>;
     static constexpr int kEpiOffset = kStages * kStageBytes;
     static constexpr int kBarrierOffset = kEpiOffset + Epi::L::kBytes;
     static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
@@ -1524,7 +1515,7 @@ struct MxTile {
     static constexpr int kEpiWarps = 16;
     static constexpr int kThreadsPerCta = 64 + 32 * kEpiWarps;
     static constexpr int kEpiAreas = AROWS == kBM ? kEpiWarps : kEpiWarps / 2;
-    using Epi = EpiWarp<kEpiAreas, 1, false, kChunk>;
+    using Epi = EpiWarp<kEpiAreas, false, kChunk>;
     // as many stages as fit beside the epilogue's, at most 12: 5 at BN 128, 4
     // at 64, 3 with four 64-row k-tiles
     static constexpr int kBudget = 227 * 1024 - 1024 - 512 - Epi::L::kBytes;
@@ -2040,7 +2031,7 @@ struct MxPairTile {
     static constexpr uint32_t kSfbCol = kSfaCol + 4;             // 484 .. 491
     // full / empty per stage, full / empty per accumulator, overlap, drain
     static constexpr int kBarriers = 2 * kStages + 4 + 1 + 1;
-    using Epi = EpiWarp<kPairEpiWarps, kPairBoxes, false, kPairChunk>;
+    using Epi = EpiWarp<kPairEpiWarps, false, kPairChunk>;
     static constexpr int kEpiOffset = kStages * kStageStride;
     static constexpr int kBarrierOffset = kEpiOffset + Epi::L::kBytes;
     static constexpr int kSmemBytes = 1024 + kBarrierOffset + kBarriers * 8 + 16;
@@ -2322,8 +2313,8 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int b
            CUDA_SUCCESS;
 }
 
-// The bf16 output or residual [M, N] in the epilogue's boxes (`chunk` columns x
-// 32 rows, 128-byte swizzle).
+// The bf16 output or residual [M, N] in the epilogue's boxes: `chunk` columns x
+// 32 rows, swizzled over the box's row (64 columns 128 bytes, 32: 64, 16: 32).
 bool make_box_map(CUtensorMap* map, const void* base, const GemmArgs& g, int chunk) {
     EncodeTiled fn = encode_tiled();
     if (fn == nullptr) return false;
@@ -2332,7 +2323,7 @@ bool make_box_map(CUtensorMap* map, const void* base, const GemmArgs& g, int chu
     const cuuint32_t box[2] = {(cuuint32_t)chunk, 32};
     const cuuint32_t elem[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box,
-              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, 
+              elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
               chunk == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
               : chunk == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                             : CU_TENSOR_MAP_SWIZZLE_32B,
