@@ -234,6 +234,13 @@ __host__ __device__ constexpr uint32_t f8_idesc(int bn) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// (the bounds-checking build) `count` values from offset `at` on lie in the
+// output, and so in the residual.
+[[maybe_unused]] __device__ __forceinline__ bool in_output(const GemmArgs& g, int64_t at,
+                                                           int count) {
+    return at >= 0 && at + count <= (int64_t)g.M * g.N;
+}
+
 // (y * a) * b, both products rounded.  The second is two scalar products: a
 // packed one whose result goes into a packed sum is compiled into one fused
 // multiply-add (also where both are written as .rn; measured), which would
@@ -476,7 +483,14 @@ struct EpiWarp {
 
   private:
     __device__ __forceinline__ bool inside(int row0, int n) const {
-        return row0 < g.M && n < g.N && RRF_IN_BOUNDS(row0 >= 0 && n >= 0, g.err);
+        return row0 < g.M && n < g.N && RRF_IN_BOUNDS(fits(row0, n), g.err);
+    }
+
+    // (the bounds-checking build) The box begins inside the output, on a box's
+    // corner (the copies' 16-byte rule), and lies on its swizzle's period.
+    [[maybe_unused]] __device__ __forceinline__ bool fits(int row0, int n) const {
+        return row0 >= 0 && n >= 0 && row0 % 32 == 0 && n % CHUNK == 0 &&
+               in_output(g, (int64_t)row0 * g.N + n, 1) && smem_u32(box) % 1024 == 0;
     }
 
     __device__ __forceinline__ void load_box(int row0, int n) {
@@ -1143,7 +1157,8 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
                 if (EPI && g.residual != nullptr) {
 #pragma unroll
                     for (int m = 0; m < NA; ++m)
-                        if (m < g.M) res[m] = ld_residual(g.residual + (int64_t)m * g.N + n);
+                        if (m < g.M && RRF_IN_BOUNDS(in_output(g, (int64_t)m * g.N + n, 1), g.err))
+                            res[m] = ld_residual(g.residual + (int64_t)m * g.N + n);
                 }
             }
             bool have = epilogue_wait(&acc_full[buf], (j >> 1) & 1, g);
@@ -1171,7 +1186,7 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
                     y[m].y = __fadd_rn(v[2 * m + 1], comb[(2 * m + 1) * T::kWRows + w]);
                 }
                 mbar_arrive(comb_empty);
-                if (ok && n < g.N && RRF_IN_BOUNDS(n >= 0, g.err)) {
+                if (ok && n < g.N) {
 #pragma unroll
                     for (int m = 0; m < NA / 2; ++m) {
                         if constexpr (!MX) {
@@ -1185,7 +1200,7 @@ __global__ void __launch_bounds__(SwapPairTile<NA, Z, MX>::kThreadsPerCta, 1)
                     if constexpr (EPI) activate_all<NA / 2>(g.act, y);
 #pragma unroll
                     for (int m = 0; m < NA; ++m) {
-                        if (m < g.M) {
+                        if (m < g.M && RRF_IN_BOUNDS(in_output(g, (int64_t)m * g.N + n, 1), g.err)) {
                             float z = m % 2 ? y[m / 2].y : y[m / 2].x;
                             if (EPI && g.residual != nullptr)
                                 z = __fadd_rn(z, __uint_as_float((uint32_t)res[m] << 16));
@@ -1895,7 +1910,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         have = __all_sync(0xFFFFFFFFu, have);
         if (!have && lane == 0) set_in_cluster(failed, split);
         tc_fence_after_sync();
-        if (quarter * 32 < AROWS && m0 + quarter * 32 < g.M && have) {
+        if (quarter * 32 < AROWS && m0 + quarter * 32 < g.M && have &&
+            RRF_IN_BOUNDS(rank < split && row < AROWS && row / own < split &&
+                              (rank * own + row % own) * T::kPitch + BN <= AROWS * T::kPitch,
+                          g.err)) {
             const uint32_t to = peer_smem(
                 parts + (rank * own + row % own) * T::kPitch, (uint32_t)(row / own));
 #pragma unroll
@@ -1926,8 +1944,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = (int)threadIdx.x - 64; i < own * (BN / 8); i += kThreads - 64) {
         const int r = i / (BN / 8), c = i % (BN / 8) * 8;
         const int row = m0 + rank * own + r, n = n0 + c;
-        if (row >= g.M || n >= g.N || !RRF_IN_BOUNDS(row >= 0 && n >= 0, g.err)) continue;
+        if (row >= g.M || n >= g.N) continue;
         const int64_t at = (int64_t)row * g.N + n;
+        if (!RRF_IN_BOUNDS(in_output(g, at, 8) && r < own && split * own <= AROWS, g.err)) continue;
         uint4 res = make_uint4(0, 0, 0, 0);
         if (g.residual != nullptr) res = ld_residual(reinterpret_cast<const uint4*>(g.residual + at));
         float2 y[4];

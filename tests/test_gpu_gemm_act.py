@@ -358,3 +358,60 @@ def test_a_wait_that_ran_out_stores_nothing(rrf, m, n, k, kernel, mx):
     assert rrf.rrf_device_error(clear=True) & rrf.RRF_DEVICE_ERROR_GEMM_TIMEOUT
     assert bool((out == 7).all())
     check(p, call(rrf, p, "silu", out=out), "silu", p["residual"])
+
+
+# small cases of every kernel of the planner, with a last stage of fewer bytes
+# (K % 128 != 0) where there is one
+CHECKED = [(5, 256, 128, "swap", 8, False), (14, 272, 256, "swap", 16, False),
+           (30, 336, 384, "swap", 32, False), (5, 256, 144, "tile", 64, False),
+           (64, 5120, 528, "tile", 64, False), (50, 16400, 1136, "tile", 64, False),
+           (37, 272, 112, "tile", 64, False),
+           (200, 272, 112, "tile", 128, False), (200, 272, 400, "tile", 128, False),
+           (250, 7184, 272, "tile", 128, False), (700, 9488, 128, "pair", 256, False),
+           (24, 336, 1552, "split", 32, False), (8, 912, 4240, "split", 32, False),
+           (40, 1040, 3216, "split", 64, False), (129, 336, 4368, "split", 128, False),
+           (1, 256, 128, "swap", 8, True), (16, 208, 512, "swap", 16, True),
+           (29, 336, 384, "swap", 32, True), (60, 1040, 384, "tile", 64, True),
+           (33, 16400, 640, "tile", 64, True), (200, 272, 384, "tile", 128, True),
+           (250, 7184, 256, "tile", 128, True), (700, 9488, 128, "pair", 256, True),
+           (20, 4624, 1536, "split", 32, True), (40, 1104, 3200, "split", 64, True),
+           (129, 336, 4352, "split", 128, True)]
+
+_CHECKED = r'''
+import sys
+sys.path[:0] = [ROOT, HERE]
+import reduce_rmsnorm_fp8_b200 as rrf
+import test_gpu_gemm_act as t
+assert rrf.LIB_PATH.endswith("librrf_debug.so"), rrf.LIB_PATH
+rrf.rrf_device_error(clear=True)
+for m, n, k, kernel, rows, mx in t.CHECKED:
+    p = t.problem(rrf, m + n, m, n, k, mx)
+    t.check(p, t.call(rrf, p, "gelu"), "gelu", p["residual"], "residual")
+    keep = p["residual"].clone()
+    t.check(p, t.call(rrf, p, "silu", out=p["residual"]), "silu", keep, "in place")
+    p["residual"] = None
+    t.check(p, t.call(rrf, p, "none"), "none", None, "no residual")
+    plain = rrf.rrf_scaled_mm_mxfp8 if mx else rrf.rrf_scaled_mm_fp8
+    t.check(p, plain(p["a"], p["sa"], p["b"], p["sb"], p["bias"]), "none", None, "plain")
+assert rrf.rrf_device_error() == 0, rrf.rrf_device_error()
+print("checked build clean")
+'''
+
+
+def test_bounds_checking_build(rrf):
+    """Every kernel of the planner in the bounds-checking build: right, with a
+    clear error word."""
+    import os
+    import subprocess
+    import sys
+    from reduce_rmsnorm_fp8_b200 import build
+    for m, n, k, kernel, rows, mx in CHECKED:
+        plan = rrf.rrf_plan_scaled_mm_act(m, n, k, SMS, mx=mx)
+        assert (plan["kernel"], plan["a_rows"]) == (kernel, rows), (m, n, k, mx, plan)
+    build.build(debug=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    root = os.path.dirname(here)
+    p = subprocess.run([sys.executable, "-c", f"ROOT = {root!r}\nHERE = {here!r}\n" + _CHECKED],
+                       env=dict(os.environ, RRF_DEBUG_LIBRARY="1"), cwd=root,
+                       capture_output=True, text=True, timeout=600)
+    assert p.returncode == 0 and "checked build clean" in p.stdout, (p.stdout + p.stderr)[-4000:]
