@@ -415,3 +415,38 @@ def test_bounds_checking_build(rrf):
                        env=dict(os.environ, RRF_DEBUG_LIBRARY="1"), cwd=root,
                        capture_output=True, text=True, timeout=600)
     assert p.returncode == 0 and "checked build clean" in p.stdout, (p.stdout + p.stderr)[-4000:]
+
+
+def check_all(p, got, act, residual, label=""):
+    """check() on every row, 512 at a time."""
+    for r in range(0, p["m"], 512):
+        rows = slice(r, min(r + 512, p["m"]))
+        part = {**p, "m": rows.stop - r, "ad": p["ad"][rows]}
+        check(part, got[rows], act, None if residual is None else residual[rows],
+              f"{label} rows {r}..")
+
+
+@pytest.mark.parametrize("m,n,k,kernel,columns,mx", [
+    (2000, 2576, 8208, "pair", 256, False), (4096, 8192, 1040, "pair", 256, False),
+    (4096, 4096, 2048, "pair", 256, False), (4096, 4096, 2048, "pair", 256, True),
+    (2000, 8208, 2176, "pair", 256, True), (4096, 4096, 512, "tile", 128, True),
+    (3000, 2064, 256, "tile", 128, False), (3000, 2064, 256, "tile", 128, True),
+    (4096, 4096, 512, "tile", 128, False), (1999, 2576, 1024, "tile", 128, True),
+    (700, 9488, 128, "pair", 256, True), (700, 9488, 128, "pair", 256, False)])
+def test_every_row(rrf, m, n, k, kernel, columns, mx):
+    """Every row of the products whose blocks take several tiles: each warp's
+    box and barrier in turn, both accumulators; with and without a residual,
+    in place, and the plain product, which has the same epilogue."""
+    plan = rrf.rrf_plan_scaled_mm_act(m, n, k, SMS, mx=mx)
+    assert (plan["kernel"], plan["tile_n"]) == (kernel, columns), plan
+    assert plan["tiles"] > plan["ctas"] // (2 if kernel == "pair" else 1), plan
+    p = problem(rrf, m + k, m, n, k, mx)
+    keep = p["residual"]
+    check_all(p, call(rrf, p, "gelu"), "gelu", keep, "residual")
+    p["residual"] = keep.clone()
+    out = call(rrf, p, "silu", out=p["residual"])
+    check_all(p, out, "silu", keep, "in place")
+    p["residual"] = None
+    check_all(p, call(rrf, p, "relu"), "relu", None, "no residual")
+    plain = rrf.rrf_scaled_mm_mxfp8 if mx else rrf.rrf_scaled_mm_fp8
+    check_all(p, plain(p["a"], p["sa"], p["b"], p["sb"], p["bias"]), "none", None, "plain")
