@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -39,9 +40,16 @@ void need(bool ok, const char* name, const char* what) {
     if (!ok) throw Refused(std::string(name) + " must be " + what);
 }
 
+// (These calls have no backward pass and are not seen by torch's dispatcher: a
+// tensor whose gradient autograd would record is refused, not dropped from the
+// graph without a word.)
 const at::Tensor& tensor(PyObject* o, const char* name) {
     need(THPVariable_Check(o), name, "a tensor");
-    return THPVariable_Unpack(o);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    need(!t.requires_grad() || !at::GradMode::is_enabled(), name,
+         "a tensor that does not require grad (this call has no gradient; call it under "
+         "torch.no_grad())");
+    return t;
 }
 
 // A tensor or None (an undefined one).

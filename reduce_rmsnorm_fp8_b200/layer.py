@@ -3,6 +3,9 @@ products with their epilogue, the per-head norm and rotation, and the paged
 FP8 cache of keys and values.  The checks and the marshalling are in C++
 (csrc/rrf_torch.cpp, built in-tree as _rrf_torch.so): these calls are short,
 and a call's own time counts.
+
+The calls have no gradient.  Where autograd records (outside torch.no_grad()),
+a tensor that requires grad is refused.
 """
 from __future__ import annotations
 

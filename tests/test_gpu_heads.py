@@ -572,6 +572,24 @@ def test_refusals_of_tensors(rrf):
         assert torch.equal(a, b)
 
 
+def test_parameters_need_no_grad(rrf):
+    """A gamma that is a parameter: refused where autograd records, and the
+    same result as its values under no_grad and in inference mode."""
+    q, k, v, qg, kg, table, pos = problem(3, 5, 2, 1, 64, 64)
+    w = torch.nn.Parameter(qg.clone())
+    want = rrf.rrf_qk_norm_rope(q, k, qg, kg, 1e-6, 0.0, table, pos)
+    with pytest.raises(ValueError, match="q_gamma must be .*require grad"):
+        rrf.rrf_qk_norm_rope(q, k, w, kg, 1e-6, 0.0, table, pos)
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            got = rrf.rrf_qk_norm_rope(q, k, w, kg, 1e-6, 0.0, table, pos)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    cache = new_cache(gen(1), 4, 16, 1, 64)
+    cache[1].requires_grad_()
+    with pytest.raises(ValueError, match="k_scales must be .*require grad"):
+        rrf.rrf_kv_cache_write_fp8(k, v, pos[:5] % 64, *cache)
+
+
 def test_empty_calls(rrf):
     q, k, v, qg, kg, table, pos = problem(1, 1, 2, 1, 64, 64)
     cache = new_cache(gen(1), 2, 16, 1, 64)

@@ -237,3 +237,35 @@ def test_constants_match_the_header(rrf):
     for name in ("RRF_DEVICE_ERROR_INDEX", "RRF_MAX_HEAD_DIM"):
         assert getattr(rrf, name) == int(re.search(rf"#define {name} (\d+)u?", text).group(1))
     assert ctypes.sizeof(rrf.RrfKvCache) == 4 * 8 + 2 * 8 + 6 * 8
+
+
+def test_tensors_that_require_grad_are_refused(rrf):
+    """Where autograd records, before anything else of the tensor is looked at;
+    under no_grad the next check speaks (these are CPU tensors)."""
+    import torch
+    x = torch.zeros((2, 2, 64), dtype=torch.bfloat16)
+    w = torch.zeros((2, 2, 64), dtype=torch.bfloat16, requires_grad=True)
+    gamma = torch.zeros(64, dtype=torch.bfloat16)
+    slots = torch.zeros(2, dtype=torch.int64)
+    codes = torch.zeros((1, 16, 2, 64), dtype=torch.uint8).view(torch.float8_e4m3fn)
+    scales = torch.zeros((1, 16, 2))
+    a, row = torch.zeros((2, 128)).to(torch.float8_e4m3fn), torch.ones(2)
+    square = torch.zeros((2, 2), dtype=torch.bfloat16, requires_grad=True)
+    for call, name in (
+            (lambda: rrf.rrf_qk_norm_rope(w, x, gamma, gamma, 1e-6, 0.0, None, None), "q"),
+            (lambda: rrf.rrf_qk_norm_rope(x, w, gamma, gamma, 1e-6, 0.0, None, None), "k"),
+            (lambda: rrf.rrf_kv_cache_write_fp8(x, w, slots, codes, scales, codes, scales), "v"),
+            (lambda: rrf.rrf_qk_norm_rope_kv_cache_fp8(x, x, w, gamma, gamma, 1e-6, 0.0, None,
+                                                       None, slots, codes, scales, codes,
+                                                       scales), "v"),
+            (lambda: rrf.rrf_scaled_mm_fp8_act(a, row.clone().requires_grad_(), a, row),
+             "a_scale"),
+            (lambda: rrf.rrf_scaled_mm_fp8_act(a, row, a, row, bias=square[0]), "bias"),
+            (lambda: rrf.rrf_scaled_mm_fp8_act(a, row, a, row, residual=square), "residual"),
+            (lambda: rrf.rrf_scaled_mm_mxfp8_act(a, row, a, row, out=square), "out"),
+            (lambda: rrf.rrf_kv_cache_read_fp8(codes, scales, codes, scales, slots.int()[None],
+                                               slots.int(), w, x), "k_out")):
+        with pytest.raises(ValueError, match=f"^{name} must be .*require grad"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):
+            call()
