@@ -76,6 +76,11 @@ int truth(PyObject* o) {
     return v;
 }
 
+// The call has written t: autograd, which may have saved it, is to know.
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 bool on(const at::Tensor& t, int index) { return t.is_cuda() && t.get_device() == index; }
 
 // A dense vector of n values (any shape).
@@ -185,7 +190,9 @@ PyObject* scaled_mm(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
                 return f_mm_fp8(a.data_ptr(), static_cast<const float*>(pa), b.data_ptr(),
                                 static_cast<const float*>(pb), pbias, act, pres, po, m, n, k, s);
         });
-        return ok ? THPVariable_Wrap(out) : nullptr;
+        if (!ok) return nullptr;
+        written(out);
+        return THPVariable_Wrap(out);
     });
 }
 
@@ -253,6 +260,11 @@ rrf_kv_cache cache_of(PyObject* const* v, int64_t n, int64_t dim, int index) {
     return c;
 }
 
+// (k_cache, k_scales, v_cache, v_scales), looked at before
+void written_cache(PyObject* const* v) {
+    for (int i = 0; i < 4; ++i) written(THPVariable_Unpack(v[i]));
+}
+
 const at::Tensor& heads_tensor(PyObject* o, const char* name) {
     const at::Tensor& t = tensor(o, name);
     need(t.dim() == 3, name, "[tokens, heads, head_dim]");
@@ -280,6 +292,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
                               norm.interleaved, norm.positions, t, hq, hk, d, s);
             }))
             return nullptr;
+        written(qo);
+        written(ko);
         PyObject* a = THPVariable_Wrap(qo);
         PyObject* b = THPVariable_Wrap(ko);
         PyObject* pair = a && b ? PyTuple_Pack(2, a, b) : nullptr;
@@ -305,6 +319,7 @@ PyObject* kv_cache_write(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
                                &cache, t, h, d, s);
             }))
             return nullptr;
+        written_cache(v + 3);
         Py_RETURN_NONE;
     });
 }
@@ -333,7 +348,10 @@ PyObject* qk_norm_rope_kv_cache(PyObject*, PyObject* const* v, Py_ssize_t nargs)
                            norm.eps, norm.weight_offset, norm.cos_sin, norm.rows, norm.rot,
                            norm.interleaved, norm.positions, slots, ub, &cache, t, hq, hk, d, s);
         });
-        return ok ? THPVariable_Wrap(qo) : nullptr;
+        if (!ok) return nullptr;
+        written(qo);
+        written_cache(v + 11);
+        return THPVariable_Wrap(qo);
     });
 }
 
@@ -362,6 +380,8 @@ PyObject* kv_cache_read(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
                               vo.data_ptr(), rows, h, d, s);
             }))
             return nullptr;
+        written(ko);
+        written(vo);
         return PyTuple_Pack(2, v[6], v[7]);
     });
 }

@@ -450,3 +450,12 @@ def test_every_row(rrf, m, n, k, kernel, columns, mx):
     check_all(p, call(rrf, p, "relu"), "relu", None, "no residual")
     plain = rrf.rrf_scaled_mm_mxfp8 if mx else rrf.rrf_scaled_mm_fp8
     check_all(p, plain(p["a"], p["sa"], p["b"], p["sb"], p["bias"]), "none", None, "plain")
+
+
+def test_written_outputs_count_a_version(rrf):
+    for mx in (False, True):
+        p = problem(rrf, 2, 4, 64, 128, mx)
+        for out in (torch.empty_like(p["residual"]), p["residual"]):
+            before = out._version
+            call(rrf, p, "silu", out=out)
+            assert out._version > before

@@ -590,6 +590,39 @@ def test_parameters_need_no_grad(rrf):
         rrf.rrf_kv_cache_write_fp8(k, v, pos[:5] % 64, *cache)
 
 
+def test_written_tensors_count_a_version(rrf):
+    """Autograd learns of a tensor that a call wrote: a backward pass that had
+    saved it is refused, as after any write in place.  The inputs' versions
+    stay."""
+    q, k, v, qg, kg, table, pos = (x.contiguous() for x in problem(3, 5, 2, 1, 64, 64))
+    cache = new_cache(gen(1), 4, 16, 1, 64)
+    slots = torch.arange(5, device="cuda")
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    starts = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    block = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    ins = (q, k, v, qg, kg, table, pos, slots, starts, block)
+    for call, outs in (
+            (lambda: rrf.rrf_qk_norm_rope(q, k, qg, kg, 1e-6, 0.0, table, pos, q_out=qo,
+                                          k_out=ko), (qo, ko)),
+            (lambda: rrf.rrf_kv_cache_write_fp8(k, v, slots, *cache), cache),
+            (lambda: rrf.rrf_qk_norm_rope_kv_cache_fp8(q, k, v, qg, kg, 1e-6, 0.0, table, pos,
+                                                       slots, *cache, q_out=qo), (qo, *cache)),
+            (lambda: rrf.rrf_kv_cache_read_fp8(*cache, block, starts, qo[:, :1].contiguous(),
+                                               ko), (ko,))):
+        before, kept = [t._version for t in outs], [t._version for t in ins]
+        call()
+        assert all(t._version > n for t, n in zip(outs, before))
+        assert [t._version for t in ins] == kept
+    x = torch.ones(q.shape, device="cuda", requires_grad=True)
+    y = x * q
+    rrf.rrf_qk_norm_rope(q, k, qg, kg, 1e-6, 0.0, table, pos, q_out=q)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():  # (its tensors count none)
+        mine = torch.empty_like(q)
+        rrf.rrf_qk_norm_rope(q, k, qg, kg, 1e-6, 0.0, table, pos, q_out=mine)
+
+
 def test_empty_calls(rrf):
     q, k, v, qg, kg, table, pos = problem(1, 1, 2, 1, 64, 64)
     cache = new_cache(gen(1), 2, 16, 1, 64)
