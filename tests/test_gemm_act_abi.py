@@ -108,3 +108,31 @@ def test_plan_refusals(rrf):
     with pytest.raises(rrf.RrfError):
         rrf.rrf_plan_scaled_mm_act(8, 256, 1024, 1)
     assert rrf.rrf_plan_scaled_mm_act(0, 256, 1024, 148)["kernel"] is None
+
+
+def test_erfc_polynomial():
+    """The coefficients in the source: within 1.9e-6 of erfcx as they are
+    written, and rounded to fp32 within 2^-24 of each term more; and the best
+    fit: the error reaches its maximum eight times with alternating sign, which
+    no polynomial of degree 6 betters."""
+    import os
+    import re
+
+    import numpy as np
+    import torch
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "reduce_rmsnorm_fp8_b200", "csrc", "rrf_gemm.cu")).read()
+    body = text[text.index("RRF_ACT_GELU) {"):]
+    c = [float(x) for x in
+         re.findall(r"both\((-?\d\.\d+e[+-]\d+)f\)", body[:body.index("const float2 e =")])]
+    assert len(c) == 7  # from the highest power down
+    a = np.linspace(0.0, 14.0, 140001)
+    exact = torch.special.erfcx(torch.from_numpy(a) / np.sqrt(2.0)).numpy() / 2
+    t = 1 / (1 + 0.3 * a)
+    error = np.polyval(c, t) / exact - 1
+    worst = np.abs(error).max()
+    assert worst <= 1.9e-6
+    rounded = np.polyval(np.float32(c).astype(np.float64), t) / exact - 1
+    assert (np.abs(rounded) <= 1.9e-6 + 2.0 ** -24 * np.polyval(np.abs(c), t) / exact).all()
+    runs = np.split(error, np.flatnonzero(np.diff(np.sign(error))) + 1)
+    assert len(runs) == 8 and all(np.abs(r).max() >= 0.985 * worst for r in runs)
