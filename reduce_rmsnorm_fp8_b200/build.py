@@ -7,7 +7,8 @@ Every CUDA translation unit under ``csrc/`` is compiled by nvcc for
 bound, in parallel) and linked into ``reduce_rmsnorm_fp8_b200/librrf.so``
 with the CUDA runtime linked statically.  ``csrc/rrf_torch.cpp``, the Python
 binding of layer.py's calls, is compiled by g++ against the installed torch
-into ``reduce_rmsnorm_fp8_b200/_rrf_torch.so``.  No GPU is needed to build.
+into ``reduce_rmsnorm_fp8_b200/_rrf_torch.so`` (left out where there is no
+torch: the C library does not need it).  No GPU is needed to build.
 
 ``--debug`` builds the bounds-checking variant, ``librrf_debug.so`` (the same
 sources with RRF_DEBUG defined: every kernel checks the indices of its global
@@ -65,11 +66,15 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs() + [__file__])
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile _rrf_torch.so unless it is newer than its sources and torch."""
+def build_binding(force: bool = False) -> str | None:
+    """Compile _rrf_torch.so unless it is newer than its sources and torch;
+    None where torch is not installed."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return None
     root = os.path.dirname(torch.__file__)
     inputs = [TORCH_SRC, os.path.join(INCLUDE, "rrf.h"), __file__, torch.version.__file__]
     if not force and os.path.exists(TORCH_LIB) and \

@@ -136,3 +136,18 @@ def test_erfc_polynomial():
     assert (np.abs(rounded) <= 1.9e-6 + 2.0 ** -24 * np.polyval(np.abs(c), t) / exact).all()
     runs = np.split(error, np.flatnonzero(np.diff(np.sign(error))) + 1)
     assert len(runs) == 8 and all(np.abs(r).max() >= 0.985 * worst for r in runs)
+
+
+def test_the_library_builds_without_torch(rrf):
+    """The C library does not need torch; only its Python binding does."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from reduce_rmsnorm_fp8_b200 import build, lib\n"
+            "assert build.build() == build.LIB and build.build_binding() is None\n"
+            "print(lib.rrf_version().decode())")
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=600)
+    assert p.returncode == 0 and p.stdout.strip() == "0.1.0", p.stdout + p.stderr
