@@ -1638,7 +1638,7 @@ __global__ void __launch_bounds__(MxTile<BN, AROWS, Z>::kThreadsPerCta, 1)
         // thread, so it counts stage and phase on, and takes every descriptor
         // as the ring's first one plus an offset (addresses stay below 2^18,
         // so the sum stays in the descriptor's address field).  B200, 512 x
-        // 1024 x 7168: 18.4 us; with descriptors built for each k-tile 21.0.
+        // 1024 x 7168: 18.7 us; with descriptors built for each k-tile 21.0.
         if (lane == 0) {
             const uint64_t a_first = kmajor_sw128_desc(smem);
             const uint64_t b_first = kmajor_sw128_desc(smem + T::kBOffset);
@@ -2624,7 +2624,9 @@ GemmPlan plan_scaled_mm(int64_t M, int64_t N, int64_t K, bool mx, int sm_count) 
 //   K split, 32 / 64 / 128 rows        0 / 0.3 / 1.7  0.21 / 0.225 / 0.25
 //                       of the k-tiles of one CTA, rounded up to its stages
 // (the operands that a CTA loads per k-tile count, hardly its products: 64
-// columns cost nearly as much as 128).  No kernel is done before e and the
+// columns cost nearly as much as 128; the MX figures of whole tiles are from
+// before their issue was made shorter, 0.02 - 0.04 a k-tile above today's).  No
+// kernel is done before e and the
 // weight's bytes at 6 TB/s.  The kernel of the least cost is taken.  K is split
 // among as many CTAs as are resident at once (of clusters of 2, 4 and 8: 74,
 // 32 and 15).  Against plan_scaled_mm's choice: 64 x 1024 x 7168 7.2 (split in
